@@ -304,6 +304,92 @@ int dit_quant_fp8_noalloc(const void* x_bf16, void* x_fp8, float* descale, long 
                           void* stream);
 
 /*
+ * dit_rms_norm - root-mean-square norm of rows with the residual's addition, ahead of a
+ * block's projections: over the C columns of each row
+ *     h = x + r,  y = h * w / sqrt(mean(h^2) + eps).
+ * Sums and h are fp32; y is rounded once, from the unrounded h, and the stream h once.
+ *
+ *   x         [rows, C] of dtype (DIT_BF16 or DIT_FP32); row i starts x_stride elements after
+ *             row i - 1 (x_stride >= C).  Every other tensor is dense.
+ *   residual  [rows, C] of dtype, or NULL (h = x).
+ *   weight    [C] of dtype, or NULL (ones).
+ *   out       [rows, C]: DIT_BF16, DIT_FP32, or DIT_FP8_E4M3 codes with scales:
+ *             descale = max|y| / 448 (1 if the maximum is 0), code = rn_satfinite(y / descale).
+ *   group     E4M3: columns of one scale, 0 (the whole row) or 128 (the last group of a row
+ *             may be shorter); otherwise 0.
+ *   descales  E4M3: [rows, 1] or [rows, ceil(C/128)] fp32, written; otherwise NULL.
+ *   stream_out  [rows, C] of dtype: h, for the next addition; NULL to skip it.  It may be the
+ *             residual itself, or x itself where x_stride = C.  Needs a residual.
+ *   rows >= 0 (0: nothing to do), C >= 1, eps >= 0.  Pointers need their element's alignment only;
+ *   rows that are 16-byte aligned and whole 16-byte pieces take a faster path.
+ */
+int dit_rms_norm(const void* x, long long x_stride, const void* residual, const void* weight, void* out,
+                 void* stream_out, float* descales, long long rows, int C, float eps, int dtype,
+                 int out_dtype, int group, void* stream);
+
+/*
+ * dit_rope_qk - rotary positions of queries and keys between the projection and the attention,
+ * with their optional per-head root-mean-square norm, in one pass: reads token-major (or any
+ * strided) bf16, writes the [B, heads, S, D] layout of the attention calls.
+ *     x' = x * w / sqrt(mean over D of x^2 + eps)                    (where a weight is given)
+ *     pair (a, b) of the first rot elements: magnitude * (a cos t - b sin t, b cos t + a sin t),
+ *     t = position * freq;  elements rot..D-1 pass unchanged.
+ *
+ *   q, k      bf16; element (b, s, h, d) at b * strides[0] + s * strides[1] + h * strides[2] + d
+ *             (q_strides, k_strides: HOST arrays of 3, multiples of 8, >= 0), so q and k can be read
+ *             out of packed [B, S, H + 2 H_kv, D] projections.  H_kv = 0 with NULL k: queries only.
+ *   q_weight, k_weight  [D] bf16, or NULL: no norm.
+ *   pos       [B, S, axes] int32 positions (pos_batch_stride elements between batches, 0 to share).
+ *   freqs     [rot / 2] fp64 on the device, radians per position of each pair (finite).  Angles are
+ *             formed in 64-bit fixed point, so positions over the whole int32 range lose nothing.
+ *   axis_pairs  HOST array of `axes` (1..3) pair counts that sum to rot / 2: pair i belongs to
+ *             the axis whose run it falls in (t, y, x grids; axes = 1 for text).
+ *   interleaved != 0: pair i is elements (2i, 2i + 1); 0: (i, i + rot / 2), rot a multiple of 16.
+ *   q_out, k_out  [B, H, S, D], [B, H_kv, S, D]: DIT_BF16, or DIT_FP8_E4M3 codes in 128-row blocks
+ *             with descales dq_blk [B, H, ceil(S/128)], dk_blk [B, H_kv, ceil(S/128)] by the rule of
+ *             dit_quant_fp8_blocks, ready for dit_attn_fwd_fp8_blocks (bf16: descales NULL).
+ *   D = 64 or 128.  B * S = 0: nothing to do.
+ */
+int dit_rope_qk(const void* q, const void* k, const long long* q_strides, const long long* k_strides,
+                const void* q_weight, const void* k_weight, float eps, const int* pos,
+                long long pos_batch_stride, const double* freqs, const int* axis_pairs, int axes, int rot,
+                int interleaved, float magnitude, void* q_out, void* k_out, float* dq_blk, float* dk_blk,
+                int B, int S, int H, int H_kv, int D, int out_dtype, void* stream);
+
+/*
+ * dit_attn_fwd_masked - attention with capped scores, a distance bias, causal, prefix and
+ * document masks, and key / value heads shared by H / H_kv query heads each.  Query i of
+ * sequence b stands at position pos = q_start[b] + i among the S_kv keys:
+ *     s_ij = scale * q_i . k_j;   softcap > 0: s_ij = softcap * tanh(s_ij / softcap);
+ *     slopes:  s_ij = s_ij - slopes[h] * |pos - j|;
+ *     key j is allowed if  (not causal, or j <= pos, or j < prefix[b])
+ *                     and  (no documents, or q_doc[b,i] = kv_doc[b,j] and q_doc[b,i] >= 0);
+ *     out_i = sum over allowed j of softmax(s_ij) v_j,   lse_i = log sum over allowed j of exp(s_ij).
+ * A query with no allowed key gets out = 0 and lse = -inf.  What the rows of K and V that a query
+ * may not attend to hold (infinities and NaN too) does not reach that query's result.
+ *
+ *   q, out    [B,H,S_q,D] bf16;  k, v  [B,H_kv,S_kv,D] bf16;  lse [B,H,S_q] fp32 or NULL.
+ *   softcap   0: scores are not capped.   slopes  [H] fp32 device or NULL.
+ *   q_start   [B] int32 device, or NULL: S_kv - S_q (the queries are the last S_q positions).
+ *             With causal != 0 a cache of S_kv rows may so hold sequences of different lengths.
+ *   prefix    [B] int32 device or NULL (0): the first keys that every query sees; needs causal.
+ *   q_doc, kv_doc  [B,S_q], [B,S_kv] int32 device, both or neither: document of each token, a
+ *             negative one for padding.  Any order; tokens of one document close together are
+ *             faster, since 128-key tiles without a key of the queries' documents are not visited.
+ *   workspace dit_attn_masked_workspace_bytes(...) bytes of device scratch, 16-byte aligned (NULL if
+ *             that is 0), contents on entry do not matter; not shared by calls that may run at
+ *             the same time.
+ *   D = 64 or 128; |q_start|, |prefix|, S_q, S_kv <= 2^30; S_q = 0 or B = 0: nothing to do;
+ *   S_kv = 0: every query is empty.  Values are finite where allowed.
+ */
+size_t dit_attn_masked_workspace_bytes(int B, int H, int H_kv, int S_q, int S_kv, int D);
+int dit_attn_fwd_masked(const void* q, const void* k, const void* v, void* out, float* lse, int B, int H,
+                        int H_kv, int S_q, int S_kv, int D, float scale, float softcap,
+                        const float* slopes, int causal, const int* q_start, const int* prefix,
+                        const int* q_doc, const int* kv_doc, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/*
  * dit_device_status - synchronises the current device, then reads the device status word
  * into *status: DIT_OK, or DIT_ERR_TIMEOUT | (site << 8) when a bounded wait inside a
  * kernel ran out (the kernel then wound down without hanging; its outputs are invalid).

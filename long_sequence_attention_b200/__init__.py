@@ -64,6 +64,12 @@ def _load() -> ctypes.CDLL:
     lib.dit_ipc_import.argtypes = [vp, ll, ctypes.POINTER(vp), ctypes.POINTER(vp)]
     lib.dit_ipc_close.argtypes = [vp]
     lib.dit_attn_fwd_fp8_blocks.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, f, i, vp]
+    lib.dit_rms_norm.argtypes = [vp, ll, vp, vp, vp, vp, vp, ll, i, f, i, i, i, vp]
+    lib.dit_rope_qk.argtypes = [vp, vp, ctypes.POINTER(ll), ctypes.POINTER(ll), vp, vp, f, vp, ll, vp, ctypes.POINTER(i),
+                                i, i, i, f, vp, vp, vp, vp, i, i, i, i, i, i, vp]
+    lib.dit_attn_masked_workspace_bytes.argtypes = [i, i, i, i, i, i]
+    lib.dit_attn_masked_workspace_bytes.restype = sz
+    lib.dit_attn_fwd_masked.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, f, f, vp, i, vp, vp, vp, vp, vp, sz, vp]
     lib.dit_status_str.argtypes = [i]
     lib.dit_status_str.restype = ctypes.c_char_p
     lib.dit_version.argtypes = []
@@ -240,6 +246,37 @@ def dit_quant_fp8_noalloc(x_bf16, x_fp8, descale, n: int, stream=None) -> None:
            "dit_quant_fp8_noalloc")
 
 
+def dit_rms_norm(x, x_stride: int, residual, weight, out, stream_out, descales, rows: int, C: int, eps: float,
+                 dtype: int = DIT_BF16, out_dtype: int = DIT_BF16, group: int = 0, stream=None) -> None:
+    _check(lib.dit_rms_norm(_ptr(x), x_stride, _ptr(residual), _ptr(weight), _ptr(out), _ptr(stream_out),
+                            _ptr(descales), rows, C, eps, dtype, out_dtype, group, _stream(stream)), "dit_rms_norm")
+
+
+def dit_rope_qk(q, k, q_strides: Sequence[int], k_strides: Optional[Sequence[int]], q_weight, k_weight, eps: float, pos,
+                pos_batch_stride: int, freqs, axis_pairs: Sequence[int], rot: int, interleaved: bool, magnitude: float,
+                q_out, k_out, dq_blk, dk_blk, B: int, S: int, H: int, H_kv: int, D: int, out_dtype: int = DIT_BF16,
+                stream=None) -> None:
+    qs = (ctypes.c_longlong * 3)(*q_strides)
+    ks = None if k_strides is None else (ctypes.c_longlong * 3)(*k_strides)
+    _check(lib.dit_rope_qk(_ptr(q), _ptr(k), qs, ks, _ptr(q_weight), _ptr(k_weight), eps, _ptr(pos), pos_batch_stride,
+                           _ptr(freqs), (ctypes.c_int * len(axis_pairs))(*axis_pairs), len(axis_pairs), rot,
+                           1 if interleaved else 0, magnitude, _ptr(q_out), _ptr(k_out), _ptr(dq_blk), _ptr(dk_blk),
+                           B, S, H, H_kv, D, out_dtype, _stream(stream)), "dit_rope_qk")
+
+
+def dit_attn_masked_workspace_bytes(B: int, H: int, H_kv: int, S_q: int, S_kv: int, D: int) -> int:
+    return int(lib.dit_attn_masked_workspace_bytes(B, H, H_kv, S_q, S_kv, D))
+
+
+def dit_attn_fwd_masked(q, k, v, out, lse, B: int, H: int, H_kv: int, S_q: int, S_kv: int, D: int, scale: float,
+                        softcap: float = 0.0, slopes=None, causal: bool = False, q_start=None, prefix=None, q_doc=None,
+                        kv_doc=None, workspace=None, workspace_bytes: int = 0, stream=None) -> None:
+    _check(lib.dit_attn_fwd_masked(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, H, H_kv, S_q, S_kv, D, scale,
+                                   softcap, _ptr(slopes), 1 if causal else 0, _ptr(q_start), _ptr(prefix), _ptr(q_doc),
+                                   _ptr(kv_doc), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "dit_attn_fwd_masked")
+
+
 def dit_device_status(clear: bool = True) -> int:
     st = ctypes.c_int(0)
     _check(lib.dit_device_status(ctypes.byref(st), 1 if clear else 0), "dit_device_status")
@@ -365,3 +402,202 @@ def quantize_fp8(x, stream=None):
     ws = torch.empty((ws_bytes // 4,), dtype=torch.float32, device=x.device)
     dit_quant_fp8(x, codes, descale, n, ws, ws_bytes, stream)
     return codes, descale
+
+
+# ------------------------------------------------- a block's other operators: norm, rotary positions, masks
+
+class _Place:
+    """The device and stream of one call: the tensors' device is made current, and `stream` (or
+    that device's current stream) too, so that outputs and scratch belong to the stream that uses them."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.device = device if device.index != torch.cuda.current_device() else None
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        self.stream = stream
+
+    def __enter__(self):
+        import torch
+        self.saved = []
+        if self.device is not None:
+            self.saved.append(torch.cuda.device(self.device))
+        if self.stream is not None:
+            self.saved.append(torch.cuda.stream(self.stream))
+        for c in self.saved:
+            c.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.saved):
+            c.__exit__(*exc)
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _like(t, name: str, dtype, shape, device) -> None:
+    """t (or None) is a dense tensor of this type, shape and device."""
+    if t is not None and not (t.dtype == dtype and tuple(t.shape) == shape and t.device == device and t.is_contiguous()):
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {list(shape)} on {device}, got "
+                         f"{t.dtype} {list(t.shape)} on {t.device}")
+
+
+def _out_code(out_dtype):
+    import torch
+    codes = {torch.bfloat16: DIT_BF16, torch.float32: DIT_FP32, torch.uint8: DIT_FP8_E4M3}
+    _need(out_dtype in codes, "out_dtype: torch.bfloat16, torch.float32 or torch.uint8 (E4M3 codes)")
+    return codes[out_dtype]
+
+
+def rms_norm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None, group: int = 0, inplace: bool = False,
+             stream=None):
+    """(y, stream, descales) of a row-wise root-mean-square norm of h = x + residual over x's last dimension.
+
+    x, weight, residual: all bf16 or all fp32.  y: x's type unless out_dtype says otherwise; torch.uint8 gives
+    E4M3 codes with fp32 descales [..., 1], or [..., ceil(C/128)] with group = 128 (else descales is None).
+    stream: h in x's type, written over residual where inplace is true; None without a residual."""
+    import torch
+    _need(x.is_cuda and x.dtype in (torch.bfloat16, torch.float32) and x.dim() >= 1 and x.shape[-1] >= 1,
+          "x: a CUDA tensor of bf16 or fp32")
+    C, shape = x.shape[-1], x.shape
+    rows = x.numel() // C
+    if x.is_contiguous():
+        ldx = C
+    else:
+        _need(x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= C,
+              "x: a contiguous tensor, or a matrix whose rows are dense")
+        ldx = x.stride(0)
+    _like(weight, "weight", x.dtype, (C,), x.device)
+    _like(residual, "residual", x.dtype, tuple(shape), x.device)
+    _need(not inplace or residual is not None, "inplace needs a residual")
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    code = _out_code(out_dtype)
+    with _Place(x.device, stream) as raw:
+        out = torch.empty(shape, dtype=out_dtype, device=x.device)
+        h = None if residual is None else residual if inplace else torch.empty(shape, dtype=x.dtype, device=x.device)
+        ds = None
+        if code == DIT_FP8_E4M3:
+            ds = torch.empty((*shape[:-1], (C + 127) // 128 if group else 1), dtype=torch.float32, device=x.device)
+        dit_rms_norm(x, ldx, residual, weight, out, h, ds, rows, C, eps,
+                     DIT_BF16 if x.dtype == torch.bfloat16 else DIT_FP32, code, group, raw)
+    return out, h, ds
+
+
+def rope_frequencies(rot: int, theta: float = 10000.0, axis_pairs: Optional[Sequence[int]] = None,
+                     scaling: str = "none", factor: float = 1.0, original_length: int = 0, fast_turns: float = 32.0,
+                     slow_turns: float = 1.0, device=None):
+    """(freqs, magnitude) for rope_qk: fp64 radians per position of the rot / 2 pairs.
+
+    Pair i of an axis of n pairs turns by theta^(-i / n) per position (axis_pairs: the pairs of each
+    axis; one axis unless given).  scaling stretches them `factor`-fold for contexts longer than trained on:
+    "linear" divides every frequency; "ntk" raises theta so that the slowest pair is divided and the fastest
+    kept; "by_parts" keeps pairs that turn more than fast_turns times within original_length, divides those
+    that turn less than slow_turns times, mixes in between, and gives the magnitude 0.1 ln(factor) + 1
+    (1 otherwise)."""
+    import math
+
+    import torch
+    _need(rot >= 2 and rot % 2 == 0, "rot: an even number of elements")
+    per = [rot // 2] if axis_pairs is None else list(axis_pairs)
+    _need(sum(per) == rot // 2 and all(n >= 0 for n in per), "axis_pairs: counts that sum to rot / 2")
+    _need(scaling in ("none", "linear", "ntk", "by_parts"), "scaling: none, linear, ntk or by_parts")
+    _need(theta > 0 and factor >= 1, "theta > 0 and factor >= 1")
+    freqs, magnitude = [], 1.0
+    for n in per:
+        base = theta
+        if scaling == "ntk" and n > 1:
+            base = theta * factor ** (n / (n - 1))
+        for i in range(n):
+            f = base ** (-i / n)
+            if scaling == "linear":
+                f /= factor
+            elif scaling == "by_parts":
+                turns = original_length * f / (2 * math.pi)
+                keep = min(1.0, max(0.0, (turns - slow_turns) / (fast_turns - slow_turns)))
+                f = f * keep + f / factor * (1.0 - keep)
+            freqs.append(f)
+    if scaling == "by_parts":
+        _need(original_length > 0 and fast_turns > slow_turns, "by_parts: original_length and fast_turns > slow_turns")
+        magnitude = 0.1 * math.log(factor) + 1.0
+    return torch.tensor(freqs, dtype=torch.float64, device=device), magnitude
+
+
+def rope_qk(q, k, pos, freqs, q_weight=None, k_weight=None, eps: float = 1e-6, axis_pairs: Optional[Sequence[int]] = None,
+            interleaved: bool = False, magnitude: float = 1.0, out_dtype=None, stream=None):
+    """(q_out, k_out, dq, dk): rotary positions of q [B, S, H, D] and k [B, S, H_kv, D] (bf16, any strides that are
+    multiples of 8 with a dense head; k may be None), normed per head first where weights [D] are given, in the
+    [B, heads, S, D] layout of the attention calls.
+
+    pos: int32 [B or 1, S, axes] (or [B or 1, S] for one axis); freqs: fp64 [rot / 2] on the device, see
+    rope_frequencies; axis_pairs: the pairs of each axis.  out_dtype torch.uint8 gives E4M3 codes in 128-row blocks
+    and their descales dq, dk, as attention_fp8_blocks takes them (otherwise dq and dk are None)."""
+    import torch
+    _need(q.is_cuda and q.dim() == 4 and q.dtype == torch.bfloat16, "q: a CUDA bf16 tensor [B, S, H, D]")
+    B, S, H, D = q.shape
+    dev = q.device
+    heads = [H]
+    if k is not None:
+        _need(k.dtype == torch.bfloat16 and k.device == dev and k.dim() == 4 and k.shape[0] == B and k.shape[1] == S
+              and k.shape[3] == D, "k: a bf16 tensor [B, S, H_kv, D] on q's device")
+        heads.append(k.shape[2])
+    for t in (q, k):
+        _need(t is None or t.stride(3) == 1, "q, k: dense heads (stride 1 along D)")
+    _like(q_weight, "q_weight", torch.bfloat16, (D,), dev)
+    _like(k_weight, "k_weight", torch.bfloat16, (D,), dev)
+    axes = 1 if pos.dim() == 2 else pos.shape[-1]
+    _need(pos.dtype == torch.int32 and pos.device == dev and pos.dim() in (2, 3) and pos.shape[0] in (1, B)
+          and pos.shape[1] == S and pos.is_contiguous(), "pos: contiguous int32 [B or 1, S, axes] on q's device")
+    _need(freqs.dtype == torch.float64 and freqs.device == dev and freqs.dim() == 1 and freqs.is_contiguous(),
+          "freqs: a contiguous fp64 vector on q's device")
+    rot = 2 * freqs.shape[0]
+    per = [rot // 2] if axis_pairs is None else axis_pairs
+    _need(len(per) == axes, "axis_pairs: one count for each axis of pos")
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    code = _out_code(out_dtype)
+    with _Place(dev, stream) as raw:
+        outs = [torch.empty((B, n, S, D), dtype=out_dtype, device=dev) for n in heads]
+        ds = [None, None]
+        if code == DIT_FP8_E4M3:
+            ds = [torch.empty((B, n, (S + 127) // 128), dtype=torch.float32, device=dev) for n in heads]
+        if k is None:
+            outs, ds, ks, H_kv = [outs[0], None], [ds[0], None], None, 0
+        else:
+            ks, H_kv = k.stride()[:3], heads[1]
+        dit_rope_qk(q, k, q.stride()[:3], ks, q_weight, k_weight, eps, pos, S * axes if pos.shape[0] == B and B > 1 else 0,
+                    freqs, per, rot, interleaved, magnitude, outs[0], outs[1], ds[0], ds[1], B, S, H, H_kv, D, code, raw)
+    return outs[0], outs[1], ds[0], ds[1]
+
+
+def masked_attention(q, k, v, scale: Optional[float] = None, softcap: float = 0.0, slopes=None, causal: bool = False,
+                     q_start=None, prefix=None, q_doc=None, kv_doc=None, with_lse: bool = True, stream=None):
+    """(out bf16, lse fp32 or None) of attention with capped scores (softcap > 0), a distance bias (slopes fp32 [H]),
+    causal, prefix (int32 [B], with causal) and document masks (int32 [B, S_q] and [B, S_kv], negative: padding).
+
+    q [B, H, S_q, D], k and v [B, H_kv, S_kv, D] bf16 with H a multiple of H_kv.  q_start int32 [B]: position of each
+    sequence's first query among the keys (S_kv - S_q unless given)."""
+    import torch
+    B, H, S_q, D = _dims(q)
+    _need(k.dim() == 4, "k: a tensor [B, H_kv, S_kv, D]")
+    H_kv, S_kv = k.shape[1], k.shape[2]
+    dev = q.device
+    _need(q.is_cuda, "q: a CUDA tensor")
+    _like(q, "q", torch.bfloat16, (B, H, S_q, D), dev)
+    _like(k, "k", torch.bfloat16, (B, H_kv, S_kv, D), dev)
+    _like(v, "v", torch.bfloat16, (B, H_kv, S_kv, D), dev)
+    _like(slopes, "slopes", torch.float32, (H,), dev)
+    _like(q_start, "q_start", torch.int32, (B,), dev)
+    _like(prefix, "prefix", torch.int32, (B,), dev)
+    _like(q_doc, "q_doc", torch.int32, (B, S_q), dev)
+    _like(kv_doc, "kv_doc", torch.int32, (B, S_kv), dev)
+    scale = (1.0 / D ** 0.5) if scale is None else scale
+    with _Place(dev, stream) as raw:
+        out = torch.empty((B, H, S_q, D), dtype=torch.bfloat16, device=dev)
+        lse = torch.empty((B, H, S_q), dtype=torch.float32, device=dev) if with_lse else None
+        n = lib.dit_attn_masked_workspace_bytes(B, H, H_kv, S_q, S_kv, D)
+        ws = torch.empty((n,), dtype=torch.uint8, device=dev) if n else None
+        dit_attn_fwd_masked(q, k, v, out, lse, B, H, H_kv, S_q, S_kv, D, scale, softcap, slopes, causal, q_start,
+                            prefix, q_doc, kv_doc, ws, n, raw)
+    return out, lse

@@ -15,6 +15,9 @@
 #include "merge.cuh"
 #include "quant.cuh"
 #include "layout.cuh"
+#include "norm.cuh"
+#include "rope.cuh"
+#include "attn_masked.cuh"
 
 namespace {
 
@@ -314,6 +317,31 @@ int grid_for(long long units, int threads, int max_blocks) {
   if (g < 1) g = 1;
   if (g > max_blocks) g = max_blocks;
   return static_cast<int>(g);
+}
+
+template <typename T, int OUT>
+int launch_norm(const NormParams& prm, cudaStream_t st) {
+  const unsigned grid = static_cast<unsigned>(std::min(prm.rows, 1LL << 20));
+  rms_norm_kernel<T, OUT><<<grid, kNormThreads, 0, st>>>(prm);
+  return cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ERR_CUDA;
+}
+
+template <bool E4M3>
+int launch_rope(const RopeParams& prm, cudaStream_t st) {
+  static std::atomic<uint64_t> attr_done{0};
+  const int rc = ensure_smem_attr(rope_kernel<E4M3>, kRopeSmem, attr_done);
+  if (rc != DIT_OK) return rc;
+  const long long grid = static_cast<long long>(prm.B) * (prm.heads[0] + prm.heads[1]) *
+                         ((prm.S + kRopeBlockRows - 1) / kRopeBlockRows);
+  rope_kernel<E4M3><<<static_cast<unsigned>(grid), 32 * kRopeWarps, kRopeSmem, st>>>(prm);
+  return cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ERR_CUDA;
+}
+
+template <int D>
+int launch_masked(const MaskedParams& prm, cudaStream_t st) {
+  const long long rows = static_cast<long long>(prm.B) * prm.H * prm.S_q;
+  attn_masked_row_kernel<D><<<grid_for(rows, kMaskedRowWarps, 1 << 20), 32 * kMaskedRowWarps, 0, st>>>(prm);
+  return cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ERR_CUDA;
 }
 
 __global__ void selftest_wait_kernel(unsigned long long timeout_ns) {
@@ -806,6 +834,184 @@ int dit_quant_fp8_noalloc(const void* x_bf16, void* x_fp8, float* descale, long 
   quant_e4m3_kernel<<<g, kQuantThreads, 0, st>>>(static_cast<const uint16_t*>(x_bf16), n, scratch, g,
                                                   static_cast<uint8_t*>(x_fp8), descale);
   return cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ERR_CUDA;
+}
+
+int dit_rms_norm(const void* x, long long x_stride, const void* residual, const void* weight, void* out,
+                 void* stream_out, float* descales, long long rows, int C, float eps, int dtype, int out_dtype,
+                 int group, void* stream) {
+  if (rows < 0 || C < 1 || x_stride < C) return DIT_ERR_INVALID_ARG;
+  if (dtype != DIT_BF16 && dtype != DIT_FP32) return DIT_ERR_INVALID_ARG;
+  if (out_dtype != DIT_BF16 && out_dtype != DIT_FP32 && out_dtype != DIT_FP8_E4M3) return DIT_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return DIT_ERR_INVALID_ARG;
+  const bool e4m3 = out_dtype == DIT_FP8_E4M3;
+  if (e4m3 ? (group != 0 && group != 128) : group != 0) return DIT_ERR_INVALID_ARG;
+  if (rows > (1LL << 40) / C || x_stride > (1LL << 40)) return DIT_ERR_INVALID_ARG;
+  if (rows == 0) return DIT_OK;
+  if (x == nullptr || out == nullptr || e4m3 != (descales != nullptr)) return DIT_ERR_INVALID_ARG;
+  if (residual == nullptr && stream_out != nullptr) return DIT_ERR_INVALID_ARG;
+  const size_t e = dtype == DIT_BF16 ? 2 : 4, oe = e4m3 ? 1 : (out_dtype == DIT_BF16 ? 2 : 4);
+  if (!aligned(x, e) || !aligned(residual, e) || !aligned(weight, e) || !aligned(stream_out, e) || !aligned(out, oe) ||
+      !aligned(descales, 4))
+    return DIT_ERR_MISALIGNED;
+  const size_t n = static_cast<size_t>(rows) * C;
+  const size_t x_bytes = (static_cast<size_t>(rows - 1) * x_stride + C) * e;
+  const long long groups = !e4m3 ? 0 : (group == 0 ? 1 : (C + group - 1) / group);
+  const size_t d_bytes = static_cast<size_t>(rows) * groups * 4;
+  if (overlaps(out, n * oe, x, x_bytes) || overlaps(out, n * oe, residual, n * e) ||
+      overlaps(out, n * oe, weight, static_cast<size_t>(C) * e) || overlaps(out, n * oe, stream_out, n * e) ||
+      overlaps(descales, d_bytes, out, n * oe) || overlaps(descales, d_bytes, x, x_bytes) ||
+      overlaps(descales, d_bytes, residual, n * e) || overlaps(descales, d_bytes, stream_out, n * e) ||
+      overlaps(descales, d_bytes, weight, static_cast<size_t>(C) * e) ||
+      overlaps(stream_out, n * e, weight, static_cast<size_t>(C) * e))
+    return DIT_ERR_INVALID_ARG;
+  // the stream may be written in place of x (dense rows) or of the residual, exactly
+  if (overlaps(stream_out, n * e, x, x_bytes) && !(stream_out == x && x_stride == C)) return DIT_ERR_INVALID_ARG;
+  if (overlaps(stream_out, n * e, residual, n * e) && stream_out != residual) return DIT_ERR_INVALID_ARG;
+  NormParams prm;
+  std::memset(&prm, 0, sizeof(prm));
+  prm.x = x; prm.x_stride = x_stride; prm.residual = residual; prm.weight = weight; prm.out = out;
+  prm.stream_out = stream_out; prm.descales = descales; prm.rows = rows; prm.C = C;
+  prm.group = group == 0 ? C : group;
+  prm.eps = eps;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool bf16 = dtype == DIT_BF16;
+  if (out_dtype == DIT_BF16) return bf16 ? launch_norm<__nv_bfloat16, 0>(prm, st) : launch_norm<float, 0>(prm, st);
+  if (out_dtype == DIT_FP32) return bf16 ? launch_norm<__nv_bfloat16, 1>(prm, st) : launch_norm<float, 1>(prm, st);
+  return bf16 ? launch_norm<__nv_bfloat16, 2>(prm, st) : launch_norm<float, 2>(prm, st);
+}
+
+int dit_rope_qk(const void* q, const void* k, const long long* q_strides, const long long* k_strides,
+                const void* q_weight, const void* k_weight, float eps, const int* pos, long long pos_batch_stride,
+                const double* freqs, const int* axis_pairs, int axes, int rot, int interleaved, float magnitude,
+                void* q_out, void* k_out, float* dq_blk, float* dk_blk, int B, int S, int H, int H_kv, int D,
+                int out_dtype, void* stream) {
+  if (B < 0 || S < 0 || H < 1 || H_kv < 0 || B > 65535 || H > 65535 || H_kv > 65535) return DIT_ERR_INVALID_ARG;
+  if (out_dtype != DIT_BF16 && out_dtype != DIT_FP8_E4M3) return DIT_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return DIT_ERR_UNSUPPORTED;
+  if (rot < 2 || rot > D || rot % 2 != 0 || axes < 1 || axes > kMaxRopeAxes || axis_pairs == nullptr)
+    return DIT_ERR_INVALID_ARG;
+  if (!interleaved && rot % 16 != 0) return DIT_ERR_UNSUPPORTED;   // the two halves are read as 16-byte pieces
+  if (!(eps >= 0.0f) || !std::isfinite(eps) || !std::isfinite(magnitude)) return DIT_ERR_INVALID_ARG;
+  RopeParams prm;
+  std::memset(&prm, 0, sizeof(prm));
+  int end = 0;
+  for (int a = 0; a < axes; ++a) {
+    if (axis_pairs[a] < 0 || axis_pairs[a] > rot / 2) return DIT_ERR_INVALID_ARG;
+    prm.axis_end[a] = end += axis_pairs[a];
+  }
+  if (end != rot / 2) return DIT_ERR_INVALID_ARG;
+  const long long tokens = static_cast<long long>(B) * S;
+  const long long nblk = (static_cast<long long>(S) + 127) / 128;
+  if (tokens * (H + H_kv) > (1LL << 33) || B * nblk * (H + H_kv) > 0x7FFFFFFFLL) return DIT_ERR_INVALID_ARG;
+  if (tokens == 0) return DIT_OK;
+  const bool e4m3 = out_dtype == DIT_FP8_E4M3;
+  if (q == nullptr || q_out == nullptr || q_strides == nullptr || pos == nullptr || freqs == nullptr)
+    return DIT_ERR_INVALID_ARG;
+  if (H_kv > 0 ? (k == nullptr || k_out == nullptr || k_strides == nullptr)
+               : (k != nullptr || k_out != nullptr || k_weight != nullptr))
+    return DIT_ERR_INVALID_ARG;
+  if (e4m3 != (dq_blk != nullptr) || (e4m3 && H_kv > 0) != (dk_blk != nullptr)) return DIT_ERR_INVALID_ARG;
+  if (pos_batch_stride != 0 && pos_batch_stride < static_cast<long long>(S) * axes) return DIT_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(q_weight, 16) ||
+      !aligned(k_weight, 16) || !aligned(pos, 4) || !aligned(freqs, 8) || !aligned(dq_blk, 4) || !aligned(dk_blk, 4))
+    return DIT_ERR_MISALIGNED;
+  const void* in[2] = {q, k};
+  void* out[2] = {q_out, k_out};
+  float* ds[2] = {dq_blk, dk_blk};
+  const int heads[2] = {H, H_kv};
+  size_t in_bytes[2] = {0, 0}, out_bytes[2] = {0, 0}, d_bytes[2] = {0, 0};
+  for (int i = 0; i < (H_kv > 0 ? 2 : 1); ++i) {
+    const long long* sd = i == 0 ? q_strides : k_strides;
+    for (int d = 0; d < 3; ++d) {
+      if (sd[d] < 0 || sd[d] > (1LL << 40)) return DIT_ERR_INVALID_ARG;
+      if (sd[d] % 8 != 0) return DIT_ERR_MISALIGNED;
+    }
+    prm.x[i] = static_cast<const __nv_bfloat16*>(in[i]);
+    prm.sb[i] = sd[0]; prm.ss[i] = sd[1]; prm.sh[i] = sd[2];
+    prm.out[i] = out[i];
+    prm.descales[i] = ds[i];
+    prm.weight[i] = static_cast<const __nv_bfloat16*>(i == 0 ? q_weight : k_weight);
+    prm.heads[i] = heads[i];
+    in_bytes[i] = static_cast<size_t>((B - 1) * sd[0] + (S - 1) * sd[1] + (heads[i] - 1) * sd[2] + D) * 2;
+    out_bytes[i] = static_cast<size_t>(tokens) * heads[i] * D * (e4m3 ? 1 : 2);
+    d_bytes[i] = e4m3 ? static_cast<size_t>(B) * heads[i] * nblk * 4 : 0;
+  }
+  const size_t pos_bytes = static_cast<size_t>((B - 1) * pos_batch_stride + static_cast<long long>(S) * axes) * 4;
+  for (int i = 0; i < 2; ++i) {
+    for (int j = 0; j < 2; ++j)
+      if (overlaps(out[i], out_bytes[i], in[j], in_bytes[j]) || overlaps(ds[i], d_bytes[i], in[j], in_bytes[j]) ||
+          overlaps(ds[i], d_bytes[i], out[j], out_bytes[j]))
+        return DIT_ERR_INVALID_ARG;
+    if (overlaps(out[i], out_bytes[i], pos, pos_bytes) || overlaps(out[i], out_bytes[i], freqs, rot / 2 * 8ull) ||
+        overlaps(out[i], out_bytes[i], q_weight, 2ull * D) || overlaps(out[i], out_bytes[i], k_weight, 2ull * D))
+      return DIT_ERR_INVALID_ARG;
+  }
+  if (overlaps(q_out, out_bytes[0], k_out, out_bytes[1]) || overlaps(dq_blk, d_bytes[0], dk_blk, d_bytes[1]))
+    return DIT_ERR_INVALID_ARG;
+  prm.pos = pos; prm.pos_sb = pos_batch_stride; prm.freqs = freqs; prm.axes = axes;
+  prm.B = B; prm.S = S; prm.D = D; prm.rot = rot; prm.interleaved = interleaved != 0;
+  prm.eps = eps; prm.magnitude = magnitude;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return e4m3 ? launch_rope<true>(prm, st) : launch_rope<false>(prm, st);
+}
+
+size_t dit_attn_masked_workspace_bytes(int B, int H, int H_kv, int S_q, int S_kv, int D) {
+  (void)B; (void)H; (void)H_kv; (void)S_q; (void)S_kv; (void)D;
+  return 0;
+}
+
+int dit_attn_fwd_masked(const void* q, const void* k, const void* v, void* out, float* lse, int B, int H, int H_kv,
+                        int S_q, int S_kv, int D, float scale, float softcap, const float* slopes, int causal,
+                        const int* q_start, const int* prefix, const int* q_doc, const int* kv_doc, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  if (B < 0 || H < 1 || H_kv < 1 || S_q < 0 || S_kv < 0 || B > 65535 || H > 65535) return DIT_ERR_INVALID_ARG;
+  if (H % H_kv != 0 || S_q > (1 << 30) || S_kv > (1 << 30)) return DIT_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return DIT_ERR_INVALID_ARG;
+  if (!(softcap >= 0.0f) || !std::isfinite(softcap)) return DIT_ERR_INVALID_ARG;
+  if ((q_doc == nullptr) != (kv_doc == nullptr)) return DIT_ERR_INVALID_ARG;
+  if (!causal && prefix != nullptr) return DIT_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return DIT_ERR_UNSUPPORTED;
+  const long long rows = static_cast<long long>(B) * H * S_q, rows_kv = static_cast<long long>(B) * H_kv * S_kv;
+  if (rows > (1LL << 33) || rows_kv > (1LL << 33)) return DIT_ERR_INVALID_ARG;
+  if (rows == 0) return DIT_OK;
+  if (q == nullptr || out == nullptr || (S_kv > 0 && (k == nullptr || v == nullptr))) return DIT_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(workspace, 16))
+    return DIT_ERR_MISALIGNED;
+  if (!aligned(lse, 4) || !aligned(slopes, 4) || !aligned(q_start, 4) || !aligned(prefix, 4) || !aligned(q_doc, 4) ||
+      !aligned(kv_doc, 4))
+    return DIT_ERR_MISALIGNED;
+  const size_t need = dit_attn_masked_workspace_bytes(B, H, H_kv, S_q, S_kv, D);
+  if (workspace_bytes < need || (need > 0 && workspace == nullptr)) return DIT_ERR_INVALID_ARG;
+  const size_t q_bytes = static_cast<size_t>(rows) * D * 2, kv_bytes = static_cast<size_t>(rows_kv) * D * 2;
+  const size_t b4 = 4ull * B;
+  const struct { const void* p; size_t n; } ins[] = {
+      {q, q_bytes}, {k, kv_bytes}, {v, kv_bytes}, {slopes, 4ull * H}, {q_start, b4}, {prefix, b4},
+      {q_doc, b4 * S_q}, {kv_doc, b4 * S_kv}};
+  const size_t lse_bytes = static_cast<size_t>(rows) * 4;
+  for (const auto& i : ins)
+    if (overlaps(out, q_bytes, i.p, i.n) || overlaps(lse, lse_bytes, i.p, i.n) || overlaps(workspace, need, i.p, i.n))
+      return DIT_ERR_INVALID_ARG;
+  if (overlaps(out, q_bytes, lse, lse_bytes) || overlaps(workspace, need, out, q_bytes) ||
+      overlaps(workspace, need, lse, lse_bytes))
+    return DIT_ERR_INVALID_ARG;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (S_kv == 0) {
+    attn_fill_empty_kernel<<<grid_for(rows * D, 256, 148 * 16), 256, 0, st>>>(out, lse, rows, D, 0);
+    return cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ERR_CUDA;
+  }
+  MaskedParams prm;
+  std::memset(&prm, 0, sizeof(prm));
+  prm.q = static_cast<const __nv_bfloat16*>(q);
+  prm.k = static_cast<const __nv_bfloat16*>(k);
+  prm.v = static_cast<const __nv_bfloat16*>(v);
+  prm.out = static_cast<__nv_bfloat16*>(out);
+  prm.lse = lse;
+  prm.B = B; prm.H = H; prm.H_kv = H_kv; prm.S_q = S_q; prm.S_kv = S_kv;
+  prm.scale = scale; prm.cap = softcap;
+  prm.slopes = slopes; prm.causal = causal != 0; prm.q_start = q_start; prm.prefix = prefix;
+  prm.q_doc = q_doc; prm.kv_doc = kv_doc;
+  prm.timeout_ns = g_timeout_ns.load();
+  return D == 64 ? launch_masked<64>(prm, st) : launch_masked<128>(prm, st);
 }
 
 int dit_device_status(int* status, int clear) {
