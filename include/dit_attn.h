@@ -379,7 +379,8 @@ int dit_rope_qk(const void* q, const void* k, const long long* q_strides, const 
  *   workspace dit_attn_masked_workspace_bytes(...) bytes of device scratch, 16-byte aligned (NULL if
  *             that is 0), contents on entry do not matter; not shared by calls that may run at
  *             the same time.
- *   D = 64 or 128; |q_start|, |prefix|, S_q, S_kv <= 2^30; S_q = 0 or B = 0: nothing to do;
+ *   D = 64 or 128; |q_start|, |prefix| < 2^30; H / H_kv * S_q, S_kv <= 2^30; scale in [1e-20, 1e20],
+ *   softcap 0 or in [1e-10, 1e10]; S_q = 0 or B = 0: nothing to do;
  *   S_kv = 0: every query is empty.  Values are finite where allowed.
  */
 size_t dit_attn_masked_workspace_bytes(int B, int H, int H_kv, int S_q, int S_kv, int D);

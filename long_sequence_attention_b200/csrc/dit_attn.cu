@@ -337,11 +337,100 @@ int launch_rope(const RopeParams& prm, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ERR_CUDA;
 }
 
-template <int D>
-int launch_masked(const MaskedParams& prm, cudaStream_t st) {
-  const long long rows = static_cast<long long>(prm.B) * prm.H * prm.S_q;
-  attn_masked_row_kernel<D><<<grid_for(rows, kMaskedRowWarps, 1 << 20), 32 * kMaskedRowWarps, 0, st>>>(prm);
-  return cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ERR_CUDA;
+// How the masked attention covers a call (host arithmetic on sizes only: the workspace is sized by it).
+// Cost model in steps of the long form (256 rows against 128 keys, about a microsecond): the long form
+// takes every KV tile of its unit in one CTA; the split form shares them between CTAs, two tiles of
+// 128 rows side by side in each, and pays for its units' start and for the join.  kMaskedSlots is the
+// SM count of a B200, a constant so that the workspace does not depend on the current device.
+constexpr int kMaskedSlots = 148;
+
+bool masked_sizes_ok(int B, int H, int H_kv, int S_q, int S_kv, int D) {
+  if (B < 0 || H < 1 || H_kv < 1 || S_q < 0 || S_kv < 0 || B > 65535 || H > 65535 || H % H_kv != 0) return false;
+  if (S_q > (1 << 30) || S_kv > (1 << 30) || (D != 64 && D != 128)) return false;
+  const long long rows = static_cast<long long>(H / H_kv) * S_q;
+  return rows <= (1LL << 30) && static_cast<long long>(B) * H * S_q <= (1LL << 33) &&
+         static_cast<long long>(B) * H_kv * S_kv <= (1LL << 33) && static_cast<long long>(B) * H <= (1LL << 22);
+}
+
+struct MaskedPlan {
+  bool split;
+  int rows, n_blk, n_split;
+  long long units;
+  size_t words_bytes, part_o_bytes, part_lse_bytes;
+  size_t total() const { return words_bytes + part_o_bytes + part_lse_bytes; }
+};
+
+MaskedPlan masked_plan(int B, int H, int H_kv, int S_q, int S_kv, int D) {
+  MaskedPlan m;
+  std::memset(&m, 0, sizeof(m));
+  const long long rows = static_cast<long long>(H / H_kv) * S_q, groups = static_cast<long long>(B) * H_kv;
+  const long long tiles = (static_cast<long long>(S_kv) + 127) / 128;
+  auto waves = [](long long units) { return static_cast<double>((units + kMaskedSlots - 1) / kMaskedSlots); };
+  const long long blk_long = (rows + 255) / 256, blk_split = (rows + 127) / 128;
+  const double cost_long = waves(groups * blk_long) * (tiles * (rows > 128 ? 1.0 : 0.7) + 2.0);
+  double best = cost_long;
+  m.split = false;
+  m.n_split = 0;
+  for (long long ns = 1; ns <= 64 && 2 * ns <= tiles && groups * blk_split * ns <= 6 * kMaskedSlots; ++ns) {
+    const long long per = (tiles + ns - 1) / ns;
+    const double cost = waves(groups * blk_split * ns) * (per * 0.6 + 2.0) + 6.0;
+    if (cost < best) {
+      best = cost;
+      m.split = true;
+      m.n_split = static_cast<int>(ns);
+    }
+  }
+  m.rows = static_cast<int>(rows);
+  m.n_blk = static_cast<int>(m.split ? blk_split : blk_long);
+  m.units = groups * m.n_blk * (m.split ? m.n_split : 1);
+  auto pad = [](size_t n) { return (n + 255) / 256 * 256; };
+  m.words_bytes = pad(static_cast<size_t>(B) * m.n_blk * ((tiles + 31) / 32) * 8);
+  if (m.split) {
+    const size_t n = static_cast<size_t>(2 * m.n_split) * groups * rows;
+    m.part_o_bytes = pad(n * D * 4);
+    m.part_lse_bytes = pad(n * 4);
+  }
+  return m;
+}
+
+template <int D, bool SPLIT>
+int launch_masked(const void* q, const void* k, const void* v, const MaskedParams& prm, cudaStream_t st) {
+  using C = MaskedCfg<D, SPLIT>;
+  // the register split waits forever unless the block is launched with what it adds up to
+  static std::atomic<int> split_state{0};   // 0 unknown, 1 ok, 2 bad
+  int state = split_state.load();
+  if (state == 0) {
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, attn_masked_kernel<D, SPLIT>) != cudaSuccess) return DIT_ERR_CUDA;
+    state = attr.numRegs == C::kRegsLaunch ? 1 : 2;
+    split_state.store(state);
+  }
+  if (state != 1) return DIT_ERR_UNSUPPORTED;
+  static std::atomic<uint64_t> attr_done{0};
+  int rc = ensure_smem_attr(attn_masked_kernel<D, SPLIT>, C::kSmemBytes, attr_done);
+  if (rc != DIT_OK) return rc;
+  MapSet<1> maps;
+  std::memset(&maps, 0, sizeof(maps));
+  const int groups = prm.B * prm.H_kv;
+  if ((rc = make_map(&maps.q[0], q, false, D, prm.rows, groups, prm.rows)) != DIT_OK) return rc;
+  if ((rc = make_map(&maps.k[0], k, false, D, prm.S_kv, groups, prm.S_kv)) != DIT_OK) return rc;
+  if ((rc = make_map(&maps.v[0], v, false, D, prm.S_kv, groups, prm.S_kv)) != DIT_OK) return rc;
+  int sms = 0;
+  if ((rc = sm_count(&sms)) != DIT_OK) return rc;
+  const int reserve = g_sm_reserve.load();
+  const int slots = sms - reserve > 1 ? sms - reserve : 1;
+  if (prm.words != nullptr) {
+    masked_tiles_kernel<SPLIT ? 128 : 256><<<prm.B * prm.n_blk, 256, 0, st>>>(prm);
+    if (cudaGetLastError() != cudaSuccess) return DIT_ERR_CUDA;
+  }
+  attn_masked_kernel<D, SPLIT><<<std::min(prm.n_units, slots), C::kThreads, C::kSmemBytes, st>>>(maps, prm);
+  if (cudaGetLastError() != cudaSuccess) return DIT_ERR_CUDA;
+  if (SPLIT) {
+    const long long n = static_cast<long long>(groups) * prm.rows;
+    masked_join_kernel<D><<<static_cast<unsigned>((n + 3) / 4), 128, 0, st>>>(prm);
+    if (cudaGetLastError() != cudaSuccess) return DIT_ERR_CUDA;
+  }
+  return DIT_OK;
 }
 
 __global__ void selftest_wait_kernel(unsigned long long timeout_ns) {
@@ -956,23 +1045,22 @@ int dit_rope_qk(const void* q, const void* k, const long long* q_strides, const 
 }
 
 size_t dit_attn_masked_workspace_bytes(int B, int H, int H_kv, int S_q, int S_kv, int D) {
-  (void)B; (void)H; (void)H_kv; (void)S_q; (void)S_kv; (void)D;
-  return 0;
+  if (!masked_sizes_ok(B, H, H_kv, S_q, S_kv, D) || B == 0 || S_q == 0 || S_kv == 0) return 0;
+  return masked_plan(B, H, H_kv, S_q, S_kv, D).total();
 }
 
 int dit_attn_fwd_masked(const void* q, const void* k, const void* v, void* out, float* lse, int B, int H, int H_kv,
                         int S_q, int S_kv, int D, float scale, float softcap, const float* slopes, int causal,
                         const int* q_start, const int* prefix, const int* q_doc, const int* kv_doc, void* workspace,
                         size_t workspace_bytes, void* stream) {
-  if (B < 0 || H < 1 || H_kv < 1 || S_q < 0 || S_kv < 0 || B > 65535 || H > 65535) return DIT_ERR_INVALID_ARG;
-  if (H % H_kv != 0 || S_q > (1 << 30) || S_kv > (1 << 30)) return DIT_ERR_INVALID_ARG;
-  if (!(scale > 0.0f) || !std::isfinite(scale)) return DIT_ERR_INVALID_ARG;
-  if (!(softcap >= 0.0f) || !std::isfinite(softcap)) return DIT_ERR_INVALID_ARG;
+  // (a scale or cap is divided by: kept well inside fp32's range)
+  if (!(scale >= 1e-20f) || !(scale <= 1e20f)) return DIT_ERR_INVALID_ARG;
+  if (softcap != 0.0f && (!(softcap >= 1e-10f) || !(softcap <= 1e10f))) return DIT_ERR_INVALID_ARG;
   if ((q_doc == nullptr) != (kv_doc == nullptr)) return DIT_ERR_INVALID_ARG;
   if (!causal && prefix != nullptr) return DIT_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return DIT_ERR_UNSUPPORTED;
+  if (!masked_sizes_ok(B, H, H_kv, S_q, S_kv, D)) return DIT_ERR_INVALID_ARG;
   const long long rows = static_cast<long long>(B) * H * S_q, rows_kv = static_cast<long long>(B) * H_kv * S_kv;
-  if (rows > (1LL << 33) || rows_kv > (1LL << 33)) return DIT_ERR_INVALID_ARG;
   if (rows == 0) return DIT_OK;
   if (q == nullptr || out == nullptr || (S_kv > 0 && (k == nullptr || v == nullptr))) return DIT_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(workspace, 16))
@@ -1001,17 +1089,22 @@ int dit_attn_fwd_masked(const void* q, const void* k, const void* v, void* out, 
   }
   MaskedParams prm;
   std::memset(&prm, 0, sizeof(prm));
-  prm.q = static_cast<const __nv_bfloat16*>(q);
-  prm.k = static_cast<const __nv_bfloat16*>(k);
-  prm.v = static_cast<const __nv_bfloat16*>(v);
+  const MaskedPlan plan = masked_plan(B, H, H_kv, S_q, S_kv, D);
+  if (plan.units > 0x7FFFFFFFLL) return DIT_ERR_INVALID_ARG;
+  char* ws = static_cast<char*>(workspace);
   prm.out = static_cast<__nv_bfloat16*>(out);
   prm.lse = lse;
   prm.B = B; prm.H = H; prm.H_kv = H_kv; prm.S_q = S_q; prm.S_kv = S_kv;
   prm.scale = scale; prm.cap = softcap;
   prm.slopes = slopes; prm.causal = causal != 0; prm.q_start = q_start; prm.prefix = prefix;
   prm.q_doc = q_doc; prm.kv_doc = kv_doc;
+  prm.rows = plan.rows; prm.n_blk = plan.n_blk; prm.n_split = plan.n_split; prm.n_units = static_cast<int>(plan.units);
+  prm.words = q_doc != nullptr ? reinterpret_cast<uint2*>(ws) : nullptr;
+  prm.part_o = reinterpret_cast<float*>(ws + plan.words_bytes);
+  prm.part_lse = reinterpret_cast<float*>(ws + plan.words_bytes + plan.part_o_bytes);
   prm.timeout_ns = g_timeout_ns.load();
-  return D == 64 ? launch_masked<64>(prm, st) : launch_masked<128>(prm, st);
+  if (plan.split) return D == 64 ? launch_masked<64, true>(q, k, v, prm, st) : launch_masked<128, true>(q, k, v, prm, st);
+  return D == 64 ? launch_masked<64, false>(q, k, v, prm, st) : launch_masked<128, false>(q, k, v, prm, st);
 }
 
 int dit_device_status(int* status, int clear) {
