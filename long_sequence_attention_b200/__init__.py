@@ -407,30 +407,32 @@ def quantize_fp8(x, stream=None):
 # ------------------------------------------------- a block's other operators: norm, rotary positions, masks
 
 class _Place:
-    """The device and stream of one call: the tensors' device is made current, and `stream` (or
-    that device's current stream) too, so that outputs and scratch belong to the stream that uses them."""
+    """The device and stream of a call that are not the current ones: within it they are, so that
+    outputs and scratch belong to the stream that uses them."""
 
     def __init__(self, device, stream):
         import torch
-        self.device = device if device.index != torch.cuda.current_device() else None
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
-        self.stream = stream
+        self.inside = [torch.cuda.device(device)] + ([] if stream is None else [torch.cuda.stream(stream)])
 
     def __enter__(self):
-        import torch
-        self.saved = []
-        if self.device is not None:
-            self.saved.append(torch.cuda.device(self.device))
-        if self.stream is not None:
-            self.saved.append(torch.cuda.stream(self.stream))
-        for c in self.saved:
+        for c in self.inside:
             c.__enter__()
-        return torch.cuda.current_stream().cuda_stream
 
     def __exit__(self, *exc):
-        for c in reversed(self.saved):
+        for c in reversed(self.inside):
             c.__exit__(*exc)
+
+
+def _elsewhere(device, stream) -> bool:
+    import torch
+    return stream is not None or device.index != torch.cuda.current_device()
+
+
+def _raw_stream(device) -> int:
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _need(ok: bool, what: str) -> None:
@@ -439,8 +441,8 @@ def _need(ok: bool, what: str) -> None:
 
 
 def _like(t, name: str, dtype, shape, device) -> None:
-    """t (or None) is a dense tensor of this type, shape and device."""
-    if t is not None and not (t.dtype == dtype and tuple(t.shape) == shape and t.device == device and t.is_contiguous()):
+    """t is a dense tensor of this type, shape and device."""
+    if not (t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()):
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {list(shape)} on {device}, got "
                          f"{t.dtype} {list(t.shape)} on {t.device}")
 
@@ -460,29 +462,35 @@ def rms_norm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None, g
     E4M3 codes with fp32 descales [..., 1], or [..., ceil(C/128)] with group = 128 (else descales is None).
     stream: h in x's type, written over residual where inplace is true; None without a residual."""
     import torch
-    _need(x.is_cuda and x.dtype in (torch.bfloat16, torch.float32) and x.dim() >= 1 and x.shape[-1] >= 1,
-          "x: a CUDA tensor of bf16 or fp32")
-    C, shape = x.shape[-1], x.shape
-    rows = x.numel() // C
-    if x.is_contiguous():
-        ldx = C
-    else:
-        _need(x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= C,
+    dt, shape = x.dtype, x.shape
+    bf16 = dt == torch.bfloat16
+    if not (x.is_cuda and (bf16 or dt == torch.float32) and shape and shape[-1]):
+        raise ValueError("x: a CUDA tensor of bf16 or fp32")
+    dev = x.device
+    if _elsewhere(dev, stream):
+        with _Place(dev, stream):
+            return rms_norm(x, weight, residual, eps, out_dtype, group, inplace)
+    C = ldx = shape[-1]
+    if not x.is_contiguous():
+        _need(len(shape) == 2 and x.stride(1) == 1 and x.stride(0) >= C,
               "x: a contiguous tensor, or a matrix whose rows are dense")
         ldx = x.stride(0)
-    _like(weight, "weight", x.dtype, (C,), x.device)
-    _like(residual, "residual", x.dtype, tuple(shape), x.device)
-    _need(not inplace or residual is not None, "inplace needs a residual")
-    out_dtype = x.dtype if out_dtype is None else out_dtype
-    code = _out_code(out_dtype)
-    with _Place(x.device, stream) as raw:
-        out = torch.empty(shape, dtype=out_dtype, device=x.device)
-        h = None if residual is None else residual if inplace else torch.empty(shape, dtype=x.dtype, device=x.device)
-        ds = None
-        if code == DIT_FP8_E4M3:
-            ds = torch.empty((*shape[:-1], (C + 127) // 128 if group else 1), dtype=torch.float32, device=x.device)
-        dit_rms_norm(x, ldx, residual, weight, out, h, ds, rows, C, eps,
-                     DIT_BF16 if x.dtype == torch.bfloat16 else DIT_FP32, code, group, raw)
+    if weight is not None:
+        _like(weight, "weight", dt, (C,), dev)
+    h = None
+    if residual is not None:
+        _like(residual, "residual", dt, shape, dev)
+        h = residual if inplace else torch.empty_like(residual)
+    elif inplace:
+        raise ValueError("inplace needs a residual")
+    code = (DIT_BF16 if bf16 else DIT_FP32) if out_dtype is None else _out_code(out_dtype)
+    out = torch.empty(shape, dtype=dt if out_dtype is None else out_dtype, device=dev)
+    ds = None
+    if code == DIT_FP8_E4M3:
+        ds = torch.empty((*shape[:-1], (C + 127) // 128 if group else 1), dtype=torch.float32, device=dev)
+    _check(lib.dit_rms_norm(x.data_ptr(), ldx, _ptr(residual), _ptr(weight), out.data_ptr(), _ptr(h), _ptr(ds),
+                            x.numel() // C, C, eps, DIT_BF16 if bf16 else DIT_FP32, code, group, _raw_stream(dev)),
+           "dit_rms_norm")
     return out, h, ds
 
 
@@ -535,40 +543,43 @@ def rope_qk(q, k, pos, freqs, q_weight=None, k_weight=None, eps: float = 1e-6, a
     rope_frequencies; axis_pairs: the pairs of each axis.  out_dtype torch.uint8 gives E4M3 codes in 128-row blocks
     and their descales dq, dk, as attention_fp8_blocks takes them (otherwise dq and dk are None)."""
     import torch
-    _need(q.is_cuda and q.dim() == 4 and q.dtype == torch.bfloat16, "q: a CUDA bf16 tensor [B, S, H, D]")
-    B, S, H, D = q.shape
+    bf16 = torch.bfloat16
+    _need(q.is_cuda and q.dim() == 4 and q.dtype == bf16, "q: a CUDA bf16 tensor [B, S, H, D]")
     dev = q.device
-    heads = [H]
+    if _elsewhere(dev, stream):
+        with _Place(dev, stream):
+            return rope_qk(q, k, pos, freqs, q_weight, k_weight, eps, axis_pairs, interleaved, magnitude, out_dtype)
+    B, S, H, D = q.shape
+    qs, ks, H_kv = q.stride(), None, 0
+    _need(qs[3] == 1, "q: dense heads (stride 1 along D)")
     if k is not None:
-        _need(k.dtype == torch.bfloat16 and k.device == dev and k.dim() == 4 and k.shape[0] == B and k.shape[1] == S
-              and k.shape[3] == D, "k: a bf16 tensor [B, S, H_kv, D] on q's device")
-        heads.append(k.shape[2])
-    for t in (q, k):
-        _need(t is None or t.stride(3) == 1, "q, k: dense heads (stride 1 along D)")
-    _like(q_weight, "q_weight", torch.bfloat16, (D,), dev)
-    _like(k_weight, "k_weight", torch.bfloat16, (D,), dev)
-    axes = 1 if pos.dim() == 2 else pos.shape[-1]
-    _need(pos.dtype == torch.int32 and pos.device == dev and pos.dim() in (2, 3) and pos.shape[0] in (1, B)
-          and pos.shape[1] == S and pos.is_contiguous(), "pos: contiguous int32 [B or 1, S, axes] on q's device")
+        H_kv, ks = k.shape[2] if k.dim() == 4 else 0, k.stride()
+        _need(k.dtype == bf16 and k.device == dev and k.shape == (B, S, H_kv, D) and ks[3] == 1,
+              "k: a bf16 tensor [B, S, H_kv, D] on q's device, with dense heads")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _like(w, name, bf16, (D,), dev)
+    ps = pos.shape
+    axes = ps[2] if len(ps) == 3 else 1
+    _need(pos.dtype == torch.int32 and pos.device == dev and len(ps) in (2, 3) and (ps[0] == B or ps[0] == 1)
+          and ps[1] == S and pos.is_contiguous(), "pos: contiguous int32 [B or 1, S, axes] on q's device")
     _need(freqs.dtype == torch.float64 and freqs.device == dev and freqs.dim() == 1 and freqs.is_contiguous(),
           "freqs: a contiguous fp64 vector on q's device")
-    rot = 2 * freqs.shape[0]
-    per = [rot // 2] if axis_pairs is None else axis_pairs
+    pairs = freqs.shape[0]
+    per = (pairs,) if axis_pairs is None else axis_pairs
     _need(len(per) == axes, "axis_pairs: one count for each axis of pos")
-    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    out_dtype = bf16 if out_dtype is None else out_dtype
     code = _out_code(out_dtype)
-    with _Place(dev, stream) as raw:
-        outs = [torch.empty((B, n, S, D), dtype=out_dtype, device=dev) for n in heads]
-        ds = [None, None]
-        if code == DIT_FP8_E4M3:
-            ds = [torch.empty((B, n, (S + 127) // 128), dtype=torch.float32, device=dev) for n in heads]
-        if k is None:
-            outs, ds, ks, H_kv = [outs[0], None], [ds[0], None], None, 0
-        else:
-            ks, H_kv = k.stride()[:3], heads[1]
-        dit_rope_qk(q, k, q.stride()[:3], ks, q_weight, k_weight, eps, pos, S * axes if pos.shape[0] == B and B > 1 else 0,
-                    freqs, per, rot, interleaved, magnitude, outs[0], outs[1], ds[0], ds[1], B, S, H, H_kv, D, code, raw)
-    return outs[0], outs[1], ds[0], ds[1]
+    q_out = torch.empty((B, H, S, D), dtype=out_dtype, device=dev)
+    k_out = None if k is None else torch.empty((B, H_kv, S, D), dtype=out_dtype, device=dev)
+    dq = dk = None
+    if code == DIT_FP8_E4M3:
+        dq = torch.empty((B, H, (S + 127) // 128), dtype=torch.float32, device=dev)
+        dk = None if k is None else torch.empty((B, H_kv, (S + 127) // 128), dtype=torch.float32, device=dev)
+    dit_rope_qk(q, k, qs[:3], None if k is None else ks[:3], q_weight, k_weight, eps, pos,
+                S * axes if ps[0] == B and B > 1 else 0, freqs, per, 2 * pairs, interleaved, magnitude, q_out, k_out,
+                dq, dk, B, S, H, H_kv, D, code, _raw_stream(dev))
+    return q_out, k_out, dq, dk
 
 
 def masked_attention(q, k, v, scale: Optional[float] = None, softcap: float = 0.0, slopes=None, causal: bool = False,
@@ -579,25 +590,29 @@ def masked_attention(q, k, v, scale: Optional[float] = None, softcap: float = 0.
     q [B, H, S_q, D], k and v [B, H_kv, S_kv, D] bf16 with H a multiple of H_kv.  q_start int32 [B]: position of each
     sequence's first query among the keys (S_kv - S_q unless given)."""
     import torch
+    bf16, i32 = torch.bfloat16, torch.int32
     B, H, S_q, D = _dims(q)
-    _need(k.dim() == 4, "k: a tensor [B, H_kv, S_kv, D]")
-    H_kv, S_kv = k.shape[1], k.shape[2]
+    _need(q.is_cuda and k.dim() == 4, "q, k: CUDA tensors [B, H, S_q, D] and [B, H_kv, S_kv, D]")
     dev = q.device
-    _need(q.is_cuda, "q: a CUDA tensor")
-    _like(q, "q", torch.bfloat16, (B, H, S_q, D), dev)
-    _like(k, "k", torch.bfloat16, (B, H_kv, S_kv, D), dev)
-    _like(v, "v", torch.bfloat16, (B, H_kv, S_kv, D), dev)
-    _like(slopes, "slopes", torch.float32, (H,), dev)
-    _like(q_start, "q_start", torch.int32, (B,), dev)
-    _like(prefix, "prefix", torch.int32, (B,), dev)
-    _like(q_doc, "q_doc", torch.int32, (B, S_q), dev)
-    _like(kv_doc, "kv_doc", torch.int32, (B, S_kv), dev)
-    scale = (1.0 / D ** 0.5) if scale is None else scale
-    with _Place(dev, stream) as raw:
-        out = torch.empty((B, H, S_q, D), dtype=torch.bfloat16, device=dev)
-        lse = torch.empty((B, H, S_q), dtype=torch.float32, device=dev) if with_lse else None
-        n = lib.dit_attn_masked_workspace_bytes(B, H, H_kv, S_q, S_kv, D)
-        ws = torch.empty((n,), dtype=torch.uint8, device=dev) if n else None
-        dit_attn_fwd_masked(q, k, v, out, lse, B, H, H_kv, S_q, S_kv, D, scale, softcap, slopes, causal, q_start,
-                            prefix, q_doc, kv_doc, ws, n, raw)
+    if _elsewhere(dev, stream):
+        with _Place(dev, stream):
+            return masked_attention(q, k, v, scale, softcap, slopes, causal, q_start, prefix, q_doc, kv_doc, with_lse)
+    H_kv, S_kv = k.shape[1], k.shape[2]
+    _like(q, "q", bf16, (B, H, S_q, D), dev)
+    _like(k, "k", bf16, (B, H_kv, S_kv, D), dev)
+    _like(v, "v", bf16, (B, H_kv, S_kv, D), dev)
+    if slopes is not None:
+        _like(slopes, "slopes", torch.float32, (H,), dev)
+    for t, name, shape in ((q_start, "q_start", (B,)), (prefix, "prefix", (B,)), (q_doc, "q_doc", (B, S_q)),
+                           (kv_doc, "kv_doc", (B, S_kv))):
+        if t is not None:
+            _like(t, name, i32, shape, dev)
+    out = torch.empty_like(q)
+    lse = torch.empty((B, H, S_q), dtype=torch.float32, device=dev) if with_lse else None
+    n = lib.dit_attn_masked_workspace_bytes(B, H, H_kv, S_q, S_kv, D)
+    ws = torch.empty((n,), dtype=torch.uint8, device=dev) if n else None
+    _check(lib.dit_attn_fwd_masked(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse), B, H, H_kv, S_q,
+                                   S_kv, D, 1.0 / D ** 0.5 if scale is None else scale, softcap, _ptr(slopes),
+                                   1 if causal else 0, _ptr(q_start), _ptr(prefix), _ptr(q_doc), _ptr(kv_doc), _ptr(ws),
+                                   n, _raw_stream(dev)), "dit_attn_fwd_masked")
     return out, lse

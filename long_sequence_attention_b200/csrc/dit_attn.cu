@@ -319,21 +319,70 @@ int grid_for(long long units, int threads, int max_blocks) {
   return static_cast<int>(g);
 }
 
-template <typename T, int OUT>
-int launch_norm(const NormParams& prm, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>(std::min(prm.rows, 1LL << 20));
-  rms_norm_kernel<T, OUT><<<grid, kNormThreads, 0, st>>>(prm);
+template <typename T, int OUT, int NV, int LANES>
+int launch_norm_vec(const NormParams& prm, int threads, cudaStream_t st) {
+  const long long per = LANES ? 256 / (LANES ? LANES : 1) : 1;
+  const long long grid = (prm.rows + per - 1) / per;
+  rms_norm_vec_kernel<T, OUT, NV, LANES><<<static_cast<unsigned>(grid), LANES ? 256 : threads, 0, st>>>(prm);
   return cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ERR_CUDA;
 }
 
-template <bool E4M3>
-int launch_rope(const RopeParams& prm, cudaStream_t st) {
-  static std::atomic<uint64_t> attr_done{0};
-  const int rc = ensure_smem_attr(rope_kernel<E4M3>, kRopeSmem, attr_done);
-  if (rc != DIT_OK) return rc;
-  const long long grid = static_cast<long long>(prm.B) * (prm.heads[0] + prm.heads[1]) *
-                         ((prm.S + kRopeBlockRows - 1) / kRopeBlockRows);
-  rope_kernel<E4M3><<<static_cast<unsigned>(grid), 32 * kRopeWarps, kRopeSmem, st>>>(prm);
+// Rows of whole aligned 16-byte pieces are held in registers as such, others as single elements.  Up to 128
+// pieces a row belongs to lanes of one warp (no block-wide steps).  Longer rows get a CTA: as few pieces
+// a thread as 1024 threads allow where the rows do not fill the GPU four times over (one pass of latency
+// counts), else 4 (loads in flight enough, and several CTAs on an SM).
+template <typename T, int OUT>
+int launch_norm(const NormParams& prm, cudaStream_t st) {
+  constexpr int N = NormVec<T>::kN;
+  constexpr uintptr_t out_align = OUT == 2 ? 4 : (OUT == 0 ? 2 * N : 16);
+  const bool fits = prm.rows <= 0x7FFFFFFFLL, few = prm.rows < 4 * 148;
+  const bool vec = prm.C % N == 0 && prm.x_stride % N == 0 && aligned(prm.x, 16) && aligned(prm.residual, 16) &&
+                   aligned(prm.weight, 16) && aligned(prm.stream_out, 16) && aligned(prm.out, out_align) &&
+                   prm.C / N <= kNormMaxVecs && fits;
+  if (!vec) {
+    const int runs = (prm.C + 127) / 128;
+    const unsigned grid = static_cast<unsigned>(std::min(prm.rows, fits && runs <= 128 ? 0x7FFFFFFFLL : 1LL << 20));
+    if (fits && runs <= 32) rms_norm_cols_kernel<T, OUT, 1><<<grid, 32 * runs, 0, st>>>(prm);
+    else if (fits && runs <= 128) rms_norm_cols_kernel<T, OUT, 4><<<grid, 32 * ((runs + 3) / 4), 0, st>>>(prm);
+    else rms_norm_kernel<T, OUT><<<grid, kNormThreads, 0, st>>>(prm);
+    return cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ERR_CUDA;
+  }
+  const int nvec = prm.C / N;
+  if (nvec <= 8) return launch_norm_vec<T, OUT, 1, 8>(prm, 256, st);
+  if (nvec <= 16) return launch_norm_vec<T, OUT, 1, 16>(prm, 256, st);
+  if (nvec <= 32) return launch_norm_vec<T, OUT, 1, 32>(prm, 256, st);
+  if (!few && nvec <= 64) return launch_norm_vec<T, OUT, 2, 32>(prm, 256, st);
+  if (!few && nvec <= kNormWarpVecs) return launch_norm_vec<T, OUT, 4, 32>(prm, 256, st);
+  auto threads = [&](int nv) { return ((nvec + nv - 1) / nv + 31) / 32 * 32; };
+  if (few && nvec <= 1024) return launch_norm_vec<T, OUT, 1, 0>(prm, threads(1), st);
+  if (few && nvec <= 2048) return launch_norm_vec<T, OUT, 2, 0>(prm, threads(2), st);
+  if (nvec <= 2048) return launch_norm_vec<T, OUT, 4, 0>(prm, threads(4), st);
+  return launch_norm_vec<T, OUT, 8, 0>(prm, threads(8), st);
+}
+
+// Heads a CTA walks over: more reuse the angles, fewer fill the GPU.  About eight CTAs' worth of work for each
+// of the SMs (two for the E4M3 form, whose CTA fills half an SM) while at most 24 heads share the angles.
+int rope_heads_per(long long token_blocks, int heads, long long ctas) {
+  const long long groups = std::min<long long>(heads, (ctas + token_blocks - 1) / token_blocks);
+  const int per = static_cast<int>((heads + groups - 1) / groups);
+  return std::min(per, 24);
+}
+
+template <int D, bool INTER>
+int launch_rope(const RopeParams& prm, bool e4m3, cudaStream_t st) {
+  const int heads = prm.heads[0] + prm.heads[1];
+  if (e4m3) {
+    const long long blocks = static_cast<long long>(prm.B) * ((prm.S + kRopeBlockRows - 1) / kRopeBlockRows);
+    const int per = rope_heads_per(blocks, heads, 148 * 3);
+    const dim3 grid(static_cast<unsigned>(blocks), (heads + per - 1) / per);
+    rope_e4m3_kernel<D, INTER><<<grid, kRopeBlockThreads, 0, st>>>(prm, per);
+  } else {
+    constexpr int kTokens = kRopeThreads * 8 / D;
+    const long long blocks = (static_cast<long long>(prm.B) * prm.S + kTokens - 1) / kTokens;
+    const int per = rope_heads_per(blocks, heads, 148 * 8);
+    const dim3 grid(static_cast<unsigned>(blocks), (heads + per - 1) / per);
+    rope_kernel<D, INTER><<<grid, kRopeThreads, 0, st>>>(prm, per);
+  }
   return cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ERR_CUDA;
 }
 
@@ -1041,7 +1090,8 @@ int dit_rope_qk(const void* q, const void* k, const long long* q_strides, const 
   prm.B = B; prm.S = S; prm.D = D; prm.rot = rot; prm.interleaved = interleaved != 0;
   prm.eps = eps; prm.magnitude = magnitude;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return e4m3 ? launch_rope<true>(prm, st) : launch_rope<false>(prm, st);
+  if (D == 64) return interleaved ? launch_rope<64, true>(prm, e4m3, st) : launch_rope<64, false>(prm, e4m3, st);
+  return interleaved ? launch_rope<128, true>(prm, e4m3, st) : launch_rope<128, false>(prm, e4m3, st);
 }
 
 size_t dit_attn_masked_workspace_bytes(int B, int H, int H_kv, int S_q, int S_kv, int D) {
