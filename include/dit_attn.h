@@ -376,14 +376,14 @@ int dit_rope_qk(const void* q, const void* k, const long long* q_strides, const 
  *   q_doc, kv_doc  [B,S_q], [B,S_kv] int32 device, both or neither: document of each token, a
  *             negative one for padding.  Any order; tokens of one document close together are
  *             faster, since 128-key tiles without a key of the queries' documents are not visited.
- *   workspace dit_attn_masked_workspace_bytes(...) bytes of device scratch, 16-byte aligned (NULL if
- *             that is 0), contents on entry do not matter; not shared by calls that may run at
+ *   workspace dit_attn_masked_workspace_bytes(..., documents given or not) bytes of device scratch,
+ *             16-byte aligned (NULL if that is 0), contents on entry do not matter; not shared by calls that may run at
  *             the same time.
  *   D = 64 or 128; |q_start|, |prefix| < 2^30; H / H_kv * S_q, S_kv <= 2^30; scale in [1e-20, 1e20],
  *   softcap 0 or in [1e-10, 1e10]; S_q = 0 or B = 0: nothing to do;
  *   S_kv = 0: every query is empty.  Values are finite where allowed.
  */
-size_t dit_attn_masked_workspace_bytes(int B, int H, int H_kv, int S_q, int S_kv, int D);
+size_t dit_attn_masked_workspace_bytes(int B, int H, int H_kv, int S_q, int S_kv, int D, int documents);
 int dit_attn_fwd_masked(const void* q, const void* k, const void* v, void* out, float* lse, int B, int H,
                         int H_kv, int S_q, int S_kv, int D, float scale, float softcap,
                         const float* slopes, int causal, const int* q_start, const int* prefix,

@@ -67,7 +67,7 @@ def _load() -> ctypes.CDLL:
     lib.dit_rms_norm.argtypes = [vp, ll, vp, vp, vp, vp, vp, ll, i, f, i, i, i, vp]
     lib.dit_rope_qk.argtypes = [vp, vp, ctypes.POINTER(ll), ctypes.POINTER(ll), vp, vp, f, vp, ll, vp, ctypes.POINTER(i),
                                 i, i, i, f, vp, vp, vp, vp, i, i, i, i, i, i, vp]
-    lib.dit_attn_masked_workspace_bytes.argtypes = [i, i, i, i, i, i]
+    lib.dit_attn_masked_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
     lib.dit_attn_masked_workspace_bytes.restype = sz
     lib.dit_attn_fwd_masked.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, f, f, vp, i, vp, vp, vp, vp, vp, sz, vp]
     lib.dit_status_str.argtypes = [i]
@@ -264,8 +264,8 @@ def dit_rope_qk(q, k, q_strides: Sequence[int], k_strides: Optional[Sequence[int
                            B, S, H, H_kv, D, out_dtype, _stream(stream)), "dit_rope_qk")
 
 
-def dit_attn_masked_workspace_bytes(B: int, H: int, H_kv: int, S_q: int, S_kv: int, D: int) -> int:
-    return int(lib.dit_attn_masked_workspace_bytes(B, H, H_kv, S_q, S_kv, D))
+def dit_attn_masked_workspace_bytes(B: int, H: int, H_kv: int, S_q: int, S_kv: int, D: int, documents: bool) -> int:
+    return int(lib.dit_attn_masked_workspace_bytes(B, H, H_kv, S_q, S_kv, D, 1 if documents else 0))
 
 
 def dit_attn_fwd_masked(q, k, v, out, lse, B: int, H: int, H_kv: int, S_q: int, S_kv: int, D: int, scale: float,
@@ -609,7 +609,7 @@ def masked_attention(q, k, v, scale: Optional[float] = None, softcap: float = 0.
             _like(t, name, i32, shape, dev)
     out = torch.empty_like(q)
     lse = torch.empty((B, H, S_q), dtype=torch.float32, device=dev) if with_lse else None
-    n = lib.dit_attn_masked_workspace_bytes(B, H, H_kv, S_q, S_kv, D)
+    n = lib.dit_attn_masked_workspace_bytes(B, H, H_kv, S_q, S_kv, D, 0 if q_doc is None else 1)
     ws = torch.empty((n,), dtype=torch.uint8, device=dev) if n else None
     _check(lib.dit_attn_fwd_masked(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse), B, H, H_kv, S_q,
                                    S_kv, D, 1.0 / D ** 0.5 if scale is None else scale, softcap, _ptr(slopes),

@@ -11,8 +11,11 @@
 //
 // The kernel keeps the pipeline of the dense forward (attn_fwd.cuh: TMA producer, one thread that
 // issues every tcgen05.mma, two softmax warpgroups, P over S in TMEM) around another walk:
-//   * The G = H / H_kv query heads of a key / value head lie next to each other in memory, so
-//     (b, key head) is one run of G * S_q query rows; a tile is 128 of them.
+//   * The query heads of a key / value head lie next to each other in memory, so they make one run
+//     of query rows cut into tiles of 128 without regard to heads, which fills the tiles of few
+//     queries; where a head's rows fill its tiles well enough, each head is a run of its own.
+//   * Units differ in length, so a CTA takes its next one from a counter when it gets there (the TMA
+//     thread fetches it early and passes it on through shared memory), the longest first.
 //   * Every role walks the same list of KV tiles of its unit: the tiles up to the last key that
 //     a row of the unit may see, without those that hold no document of its rows (bits that a
 //     small kernel writes before).  Tiles that every row sees whole take the dense path (the
@@ -44,10 +47,12 @@ struct MaskedParams {
   const int* prefix;                // [B] or null: 0
   const int* q_doc;                 // [B, S_q], with kv_doc, or null
   const int* kv_doc;                // [B, S_kv]
-  int rows;                         // query rows of one (b, key head): H / H_kv * S_q
-  int n_blk;                        // units of rows: ceil(rows / 256), split form ceil(rows / 128)
+  int run_heads, runs;              // query heads of a run (H / H_kv, or 1), runs = B * H / run_heads
+  int rows;                         // query rows of a run: run_heads * S_q
+  int n_blk;                        // units of a run's rows: ceil(rows / 256), split form ceil(rows / 128)
   int n_split;                      // split form: shares of the KV tiles
   int n_units;
+  unsigned int* next_unit;          // units handed out beyond the first of every CTA (zero at launch); null: in steps
   uint2* words;                     // [B, n_blk, ceil(S_kv / 4096)] {needed, whole} tile bits, or null
   float* part_o;                    // split form: [2 n_split, B * H * S_q, D]
   float* part_lse;                  // split form: [2 n_split, B * H * S_q]
@@ -56,9 +61,9 @@ struct MaskedParams {
 
 constexpr int kMaskedTile = 128;    // keys of a KV tile
 
-// What one unit computes: query rows r0.. of (b, key head) run bg, KV tiles [j0, j1).
+// What one unit computes: query rows r0.. of a run, KV tiles [j0, j1) of key head kv = b * H_kv + key head.
 struct MaskedUnit {
-  int bg, b, r0, start, pre;
+  int run, kv, b, r0, start, pre;
   int j0, j1;
   int n_whole;                      // keys [0, n_whole) are left by every row's causal / prefix mask
   const uint2* words;
@@ -77,13 +82,15 @@ __device__ __forceinline__ MaskedUnit masked_unit(const MaskedParams& p, int u) 
   if constexpr (SPLIT) {
     share = u % p.n_split;
     blk = (u / p.n_split) % p.n_blk;
-    w.bg = u / p.n_split / p.n_blk;
+    w.run = u / p.n_split / p.n_blk;
   } else {
-    // the last rows (of a causal mask: the longest lists) first
-    blk = p.n_blk - 1 - u % p.n_blk;
-    w.bg = u / p.n_blk;
+    // the last rows (of a causal mask: the longest lists) of every run first
+    blk = p.n_blk - 1 - u / p.runs;
+    w.run = u % p.runs;
   }
-  w.b = w.bg / p.H_kv;
+  const int per_b = p.H / p.run_heads;
+  w.b = w.run / per_b;
+  w.kv = w.b * p.H_kv + (w.run % per_b) * p.run_heads / (p.H / p.H_kv);
   w.r0 = blk * kRows;
   w.start = p.q_start ? __ldg(p.q_start + w.b) : p.S_kv - p.S_q;
   w.pre = p.prefix ? __ldg(p.prefix + w.b) : 0;
@@ -166,6 +173,7 @@ __global__ void __launch_bounds__(256) masked_tiles_kernel(const MaskedParams p)
   const bool q_one = lo == hi && !pad;
   const int* kd = p.kv_doc + static_cast<size_t>(b) * p.S_kv;
   uint2* words = p.words + static_cast<size_t>(blockIdx.x) * n_words;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.next_unit != nullptr) *p.next_unit = 0u;
   for (int w = warp; w < n_words; w += 8) {
     uint2 x = make_uint2(0u, 0u);
     for (int t = 0; t < 32; ++t) {
@@ -208,9 +216,11 @@ struct MaskedCfg {
   static constexpr int kOffIds = kOffV + kStages * kTileBytes;      // documents of the tile's keys, per V stage
   static constexpr int kOffBad = kOffIds + kStages * 512;           // 128 bits of flagged keys, per V stage
   static constexpr int kOffBar = kOffBad + kStages * 16;
-  static constexpr int kNumBars = 2 + 5 * kStages + 6 + 1;
+  static constexpr int kUnitSlots = 4;                              // units handed on and not yet taken by every role
+  static constexpr int kUnitReaders = 1 + 2 + 8;                    // MMA, V and softmax warps
+  static constexpr int kNumBars = 2 + 5 * kStages + 6 + 1 + 2 * kUnitSlots;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
-  static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+  static constexpr int kSmemBytes = kOffMisc + 16 + 4 * kUnitSlots + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
@@ -296,8 +306,11 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* bar_p_full = bar_s_full + 2;              // [2]
   uint64_t* bar_o_final = bar_p_full + 2;             // [2]
   uint64_t* bar_drain = bar_o_final + 2;
+  uint64_t* bar_u_full = bar_drain + 1;               // [kUnitSlots]
+  uint64_t* bar_u_empty = bar_u_full + C::kUnitSlots; // [kUnitSlots]
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  volatile int* units = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);
   int* ids = reinterpret_cast<int*>(smem + C::kOffIds);
   uint32_t* bad = reinterpret_cast<uint32_t*>(smem + C::kOffBad);
   uint8_t* sQ = smem;
@@ -324,6 +337,10 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(bar_o_final + t, 1);
     }
     mbar_init(bar_drain, 1);
+    for (int s = 0; s < C::kUnitSlots; ++s) {
+      mbar_init(bar_u_full + s, 1);
+      mbar_init(bar_u_empty + s, C::kUnitReaders);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -339,6 +356,15 @@ __global__ void __launch_bounds__(384, 1)
   // Q tiles of a unit that hold rows (long form; in the split form both streams use the one tile)
   auto q_tiles = [&](const MaskedUnit& w) { return SPLIT ? 1 : (p.rows - w.r0 > 128 ? 2 : 1); };
 
+  // The i-th unit of this CTA, as the TMA thread passed it on (n_units or more: no further one); < 0: gave up.
+  // Every reading warp frees the slot once.
+  auto unit_of = [&](int i) {
+    const int slot = i % C::kUnitSlots;
+    if (!mbar_wait(bar_u_full + slot, (i / C::kUnitSlots) & 1, abort_flag, tmo, 0x2D)) return -1;
+    return units[slot];
+  };
+  auto unit_taken = [&](int i) { mbar_arrive(bar_u_empty + i % C::kUnitSlots); };
+
   if (warp >= 8) {
     regs_dec<C::kRegsCtl>();
     if (warp == C::kTmaWarp) {
@@ -349,8 +375,16 @@ __global__ void __launch_bounds__(384, 1)
         tma_prefetch_desc(&maps.v[0]);
         int g = 0, nq = 0, k_issued = 0, v_issued = 0;      // running tile and Q counts
         bool ok = true;
-        for (int u = blockIdx.x; ok && u < p.n_units; u += gridDim.x) {
+        int u = blockIdx.x;
+        for (int i = 0; ok; ++i) {
+          const int slot = i % C::kUnitSlots;
+          if (i >= C::kUnitSlots && !(ok = mbar_wait(bar_u_empty + slot, ((i / C::kUnitSlots) + 1) & 1, abort_flag, tmo, 0x2E)))
+            break;
+          units[slot] = u;
+          mbar_arrive(bar_u_full + slot);
+          if (u >= p.n_units) break;
           const MaskedUnit w = masked_unit<SPLIT>(p, u);
+          u = p.next_unit ? static_cast<int>(gridDim.x + atomicAdd(p.next_unit, 1u)) : u + static_cast<int>(gridDim.x);
           MaskedTiles it(w);
           int j;
           bool part, first = true;
@@ -363,7 +397,7 @@ __global__ void __launch_bounds__(384, 1)
               for (int t = 0; t < nt; ++t)
                 for (int b = 0; b < C::kNBlk; ++b)
                   tma_load_4d(sQ + t * C::kTileBytes + b * C::kBlkBytes, &maps.q[0], bar_q_full, b * 64,
-                              w.r0 + t * 128, w.bg, 0);
+                              w.r0 + t * 128, w.run, 0);
               ++nq;
             }
             const int st = g % NS;
@@ -371,13 +405,13 @@ __global__ void __launch_bounds__(384, 1)
             mbar_arrive_expect_tx(bar_k_full + st, C::kTileBytes);
             for (int b = 0; b < C::kNBlk; ++b)
               tma_load_4d(sK + st * C::kTileBytes + b * C::kBlkBytes, &maps.k[0], bar_k_full + st, b * 64,
-                          j * kMaskedTile, w.bg, 0);
+                          j * kMaskedTile, w.kv, 0);
             k_issued = g + 1;
             if (g >= NS && !(ok = mbar_wait(bar_v_empty + st, ((g / NS) + 1) & 1, abort_flag, tmo, 0x22))) break;
             mbar_arrive_expect_tx(bar_v_full + st, C::kTileBytes);
             for (int b = 0; b < C::kNBlk; ++b)
               tma_load_4d(sV + st * C::kTileBytes + b * C::kBlkBytes, &maps.v[0], bar_v_full + st, b * 64,
-                          j * kMaskedTile, w.bg, 0);
+                          j * kMaskedTile, w.kv, 0);
             v_issued = ++g;
           }
         }
@@ -428,7 +462,10 @@ __global__ void __launch_bounds__(384, 1)
           ++np[t];
           return r;
         };
-        for (int u = blockIdx.x; ok && u < p.n_units; u += gridDim.x) {
+        for (int i = 0; ok; ++i) {
+          const int u = unit_of(i);
+          if (u < 0 || u >= p.n_units) break;
+          unit_taken(i);
           const MaskedUnit w = masked_unit<SPLIT>(p, u);
           MaskedTiles it(w);
           const int nt = q_tiles(w);
@@ -482,11 +519,11 @@ __global__ void __launch_bounds__(384, 1)
           if (n == 0) continue;
           tc_commit(bar_q_empty);                // every S MMA of this unit is issued
           if constexpr (SPLIT) {
-            for (int i = n >= 2 ? n - 2 : 0; ok && i < n; ++i) {
-              const int t = i & 1, gt = g - n + i;
+            for (int e = n >= 2 ? n - 2 : 0; ok && e < n; ++e) {
+              const int t = e & 1, gt = g - n + e;
               if (!(ok = wait_v(gt) && wait_p(t))) break;
               tc_fence_after();
-              issue_pv(t, gt % NS, i >= 2);
+              issue_pv(t, gt % NS, e >= 2);
               tc_commit(bar_o_final + t);
               tc_commit(bar_v_empty + gt % NS);
             }
@@ -512,7 +549,11 @@ __global__ void __launch_bounds__(384, 1)
       const int half = warp - C::kVWarp;
       bool ok = true;
       int g = 0;
-      for (int u = blockIdx.x; ok && u < p.n_units; u += gridDim.x) {
+      for (int i = 0; ok; ++i) {
+        const int u = unit_of(i);
+        __syncwarp();
+        if (__any_sync(0xffffffffu, u < 0 || u >= p.n_units)) break;
+        if (lane == 0) unit_taken(i);
         const MaskedUnit w = masked_unit<SPLIT>(p, u);
         MaskedTiles it(w);
         int j;
@@ -580,18 +621,21 @@ __global__ void __launch_bounds__(384, 1)
     const float unit = capped ? p.cap : p.scale;
     const float cl = unit * 1.4426950408889634f;
     const float cap_c = capped ? p.scale / p.cap : 0.0f;
-    const int G = p.H / p.H_kv;
     bool ok = true;
     int g = 0, ns = 0, no = 0;                   // running tiles of the CTA, S tiles and O's of this stream
 
-    for (int u = blockIdx.x; ok && u < p.n_units; u += gridDim.x) {
+    for (int i = 0; ok; ++i) {
+      const int u = unit_of(i);
+      __syncwarp();
+      if (__any_sync(0xffffffffu, u < 0 || u >= p.n_units)) break;
+      if (lane == 0) unit_taken(i);
       const MaskedUnit w = masked_unit<SPLIT>(p, u);
       MaskedTiles it(w);
       const bool mine = SPLIT || t < q_tiles(w);
       const int r = w.r0 + (SPLIT ? 0 : t * 128) + row;
       const bool valid_row = r < p.rows;
       const bool warp_rows = __any_sync(0xffffffffu, valid_row);
-      const int token = r % p.S_q, head = (w.bg % p.H_kv) * G + r / p.S_q;
+      const int token = r % p.S_q, head = w.run % (p.H / p.run_heads) * p.run_heads + r / p.S_q;
       const int pos = w.start + token;
       int lim = p.S_kv, doc = -1;
       float slope = 0.0f;
@@ -708,9 +752,9 @@ __global__ void __launch_bounds__(384, 1)
       const bool empty = own == 0 || l == 0.0f;                  // no key was visible
       const float inv = empty ? 0.0f : 1.0f / l;
       const float lse = empty ? -INFINITY : unit * m_use + logf(l);
-      const size_t row_idx = static_cast<size_t>(w.bg) * p.rows + r;
+      const size_t row_idx = static_cast<size_t>(w.run) * p.rows + r;
       if constexpr (SPLIT) {
-        const size_t n_rows = static_cast<size_t>(p.B) * p.H_kv * p.rows;
+        const size_t n_rows = static_cast<size_t>(p.runs) * p.rows;
         const size_t at = static_cast<size_t>(2 * (u % p.n_split) + t) * n_rows + row_idx;
         if (valid_row) p.part_lse[at] = lse;
         if (own > 0)

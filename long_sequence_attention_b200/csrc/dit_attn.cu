@@ -403,42 +403,52 @@ bool masked_sizes_ok(int B, int H, int H_kv, int S_q, int S_kv, int D) {
 
 struct MaskedPlan {
   bool split;
-  int rows, n_blk, n_split;
+  int run_heads, runs, rows, n_blk, n_split;
   long long units;
-  size_t words_bytes, part_o_bytes, part_lse_bytes;
-  size_t total() const { return words_bytes + part_o_bytes + part_lse_bytes; }
+  size_t next_bytes, words_bytes, part_o_bytes, part_lse_bytes;
+  size_t total() const { return next_bytes + words_bytes + part_o_bytes + part_lse_bytes; }
 };
 
-MaskedPlan masked_plan(int B, int H, int H_kv, int S_q, int S_kv, int D) {
+MaskedPlan masked_plan(int B, int H, int H_kv, int S_q, int S_kv, int D, bool docs) {
   MaskedPlan m;
   std::memset(&m, 0, sizeof(m));
-  const long long rows = static_cast<long long>(H / H_kv) * S_q, groups = static_cast<long long>(B) * H_kv;
   const long long tiles = (static_cast<long long>(S_kv) + 127) / 128;
   auto waves = [](long long units) { return static_cast<double>((units + kMaskedSlots - 1) / kMaskedSlots); };
-  const long long blk_long = (rows + 255) / 256, blk_split = (rows + 127) / 128;
-  const double cost_long = waves(groups * blk_long) * (tiles * (rows > 128 ? 1.0 : 0.7) + 2.0);
-  double best = cost_long;
-  m.split = false;
-  m.n_split = 0;
-  for (long long ns = 1; ns <= 64 && 2 * ns <= tiles && groups * blk_split * ns <= 6 * kMaskedSlots; ++ns) {
+  // a head is a run of its own where that leaves at most an eighth of its tiles' rows empty (a tile with the
+  // end of one head and the start of the next takes the keys of both)
+  const long long own = (S_q + 255LL) / 256 * 256;
+  const int G = H / H_kv;
+  const int pack = own - S_q <= own / 8 ? 1 : G;
+  const long long rows = static_cast<long long>(pack) * S_q, runs = static_cast<long long>(B) * H / pack;
+  const long long blk = (rows + 255) / 256;
+  double best = waves(runs * blk) * (tiles * (rows > 128 ? 1.0 : 0.7) + 2.0);
+  // the split form always packs: its calls have few rows
+  const long long rows_split = static_cast<long long>(G) * S_q, runs_split = static_cast<long long>(B) * H_kv;
+  const long long blk_split = (rows_split + 127) / 128;
+  for (long long ns = 1; ns <= 64 && 2 * ns <= tiles && runs_split * blk_split * ns <= 6 * kMaskedSlots; ++ns) {
     const long long per = (tiles + ns - 1) / ns;
-    const double cost = waves(groups * blk_split * ns) * (per * 0.6 + 2.0) + 6.0;
+    const double cost = waves(runs_split * blk_split * ns) * (per * 0.6 + 2.0) + 6.0;
     if (cost < best) {
       best = cost;
       m.split = true;
       m.n_split = static_cast<int>(ns);
     }
   }
-  m.rows = static_cast<int>(rows);
-  m.n_blk = static_cast<int>(m.split ? blk_split : blk_long);
-  m.units = groups * m.n_blk * (m.split ? m.n_split : 1);
+  m.run_heads = m.split ? G : pack;
+  m.rows = static_cast<int>(m.split ? rows_split : rows);
+  m.runs = static_cast<int>(m.split ? runs_split : runs);
+  m.n_blk = static_cast<int>(m.split ? blk_split : blk);
+  m.units = static_cast<long long>(m.runs) * m.n_blk * (m.split ? m.n_split : 1);
   auto pad = [](size_t n) { return (n + 255) / 256 * 256; };
-  m.words_bytes = pad(static_cast<size_t>(B) * m.n_blk * ((tiles + 31) / 32) * 8);
+  m.next_bytes = 256;
+  if (docs) m.words_bytes = pad(static_cast<size_t>(B) * m.n_blk * ((tiles + 31) / 32) * 8);
   if (m.split) {
-    const size_t n = static_cast<size_t>(2 * m.n_split) * groups * rows;
+    const size_t n = static_cast<size_t>(2 * m.n_split) * m.runs * m.rows;
     m.part_o_bytes = pad(n * D * 4);
     m.part_lse_bytes = pad(n * 4);
   }
+  // (no scratch for a call whose units each get a CTA of their own)
+  if (m.units <= kMaskedSlots && !docs && !m.split) m.next_bytes = 0;
   return m;
 }
 
@@ -461,21 +471,26 @@ int launch_masked(const void* q, const void* k, const void* v, const MaskedParam
   MapSet<1> maps;
   std::memset(&maps, 0, sizeof(maps));
   const int groups = prm.B * prm.H_kv;
-  if ((rc = make_map(&maps.q[0], q, false, D, prm.rows, groups, prm.rows)) != DIT_OK) return rc;
+  if ((rc = make_map(&maps.q[0], q, false, D, prm.rows, prm.runs, prm.rows)) != DIT_OK) return rc;
   if ((rc = make_map(&maps.k[0], k, false, D, prm.S_kv, groups, prm.S_kv)) != DIT_OK) return rc;
   if ((rc = make_map(&maps.v[0], v, false, D, prm.S_kv, groups, prm.S_kv)) != DIT_OK) return rc;
   int sms = 0;
   if ((rc = sm_count(&sms)) != DIT_OK) return rc;
   const int reserve = g_sm_reserve.load();
   const int slots = sms - reserve > 1 ? sms - reserve : 1;
-  if (prm.words != nullptr) {
-    masked_tiles_kernel<SPLIT ? 128 : 256><<<prm.B * prm.n_blk, 256, 0, st>>>(prm);
+  const int grid = std::min(prm.n_units, slots);
+  MaskedParams pr = prm;
+  if (pr.n_units <= grid) pr.next_unit = nullptr;
+  if (pr.words != nullptr) {
+    masked_tiles_kernel<SPLIT ? 128 : 256><<<pr.B * pr.n_blk, 256, 0, st>>>(pr);
     if (cudaGetLastError() != cudaSuccess) return DIT_ERR_CUDA;
+  } else if (pr.next_unit != nullptr) {
+    if (cudaMemsetAsync(pr.next_unit, 0, sizeof(unsigned int), st) != cudaSuccess) return DIT_ERR_CUDA;
   }
-  attn_masked_kernel<D, SPLIT><<<std::min(prm.n_units, slots), C::kThreads, C::kSmemBytes, st>>>(maps, prm);
+  attn_masked_kernel<D, SPLIT><<<grid, C::kThreads, C::kSmemBytes, st>>>(maps, pr);
   if (cudaGetLastError() != cudaSuccess) return DIT_ERR_CUDA;
   if (SPLIT) {
-    const long long n = static_cast<long long>(groups) * prm.rows;
+    const long long n = static_cast<long long>(prm.runs) * prm.rows;
     masked_join_kernel<D><<<static_cast<unsigned>((n + 3) / 4), 128, 0, st>>>(prm);
     if (cudaGetLastError() != cudaSuccess) return DIT_ERR_CUDA;
   }
@@ -1094,9 +1109,9 @@ int dit_rope_qk(const void* q, const void* k, const long long* q_strides, const 
   return interleaved ? launch_rope<128, true>(prm, e4m3, st) : launch_rope<128, false>(prm, e4m3, st);
 }
 
-size_t dit_attn_masked_workspace_bytes(int B, int H, int H_kv, int S_q, int S_kv, int D) {
+size_t dit_attn_masked_workspace_bytes(int B, int H, int H_kv, int S_q, int S_kv, int D, int documents) {
   if (!masked_sizes_ok(B, H, H_kv, S_q, S_kv, D) || B == 0 || S_q == 0 || S_kv == 0) return 0;
-  return masked_plan(B, H, H_kv, S_q, S_kv, D).total();
+  return masked_plan(B, H, H_kv, S_q, S_kv, D, documents != 0).total();
 }
 
 int dit_attn_fwd_masked(const void* q, const void* k, const void* v, void* out, float* lse, int B, int H, int H_kv,
@@ -1118,7 +1133,7 @@ int dit_attn_fwd_masked(const void* q, const void* k, const void* v, void* out, 
   if (!aligned(lse, 4) || !aligned(slopes, 4) || !aligned(q_start, 4) || !aligned(prefix, 4) || !aligned(q_doc, 4) ||
       !aligned(kv_doc, 4))
     return DIT_ERR_MISALIGNED;
-  const size_t need = dit_attn_masked_workspace_bytes(B, H, H_kv, S_q, S_kv, D);
+  const size_t need = dit_attn_masked_workspace_bytes(B, H, H_kv, S_q, S_kv, D, q_doc != nullptr);
   if (workspace_bytes < need || (need > 0 && workspace == nullptr)) return DIT_ERR_INVALID_ARG;
   const size_t q_bytes = static_cast<size_t>(rows) * D * 2, kv_bytes = static_cast<size_t>(rows_kv) * D * 2;
   const size_t b4 = 4ull * B;
@@ -1139,8 +1154,8 @@ int dit_attn_fwd_masked(const void* q, const void* k, const void* v, void* out, 
   }
   MaskedParams prm;
   std::memset(&prm, 0, sizeof(prm));
-  const MaskedPlan plan = masked_plan(B, H, H_kv, S_q, S_kv, D);
-  if (plan.units > 0x7FFFFFFFLL) return DIT_ERR_INVALID_ARG;
+  const MaskedPlan plan = masked_plan(B, H, H_kv, S_q, S_kv, D, q_doc != nullptr);
+  if (plan.units > 0x7FFF0000LL) return DIT_ERR_INVALID_ARG;
   char* ws = static_cast<char*>(workspace);
   prm.out = static_cast<__nv_bfloat16*>(out);
   prm.lse = lse;
@@ -1149,6 +1164,9 @@ int dit_attn_fwd_masked(const void* q, const void* k, const void* v, void* out, 
   prm.slopes = slopes; prm.causal = causal != 0; prm.q_start = q_start; prm.prefix = prefix;
   prm.q_doc = q_doc; prm.kv_doc = kv_doc;
   prm.rows = plan.rows; prm.n_blk = plan.n_blk; prm.n_split = plan.n_split; prm.n_units = static_cast<int>(plan.units);
+  prm.run_heads = plan.run_heads; prm.runs = plan.runs;
+  prm.next_unit = plan.next_bytes ? reinterpret_cast<unsigned int*>(ws) : nullptr;
+  ws += plan.next_bytes;
   prm.words = q_doc != nullptr ? reinterpret_cast<uint2*>(ws) : nullptr;
   prm.part_o = reinterpret_cast<float*>(ws + plan.words_bytes);
   prm.part_lse = reinterpret_cast<float*>(ws + plan.words_bytes + plan.part_o_bytes);
