@@ -64,7 +64,7 @@ constexpr int kMaskedTile = 128;    // keys of a KV tile
 // What one unit computes: query rows r0.. of a run, KV tiles [j0, j1) of key head kv = b * H_kv + key head.
 struct MaskedUnit {
   int run, kv, b, r0, start, pre;
-  int j0, j1;
+  int j0, j1, jc;                   // jc: where the walk starts
   int n_whole;                      // keys [0, n_whole) are left by every row's causal / prefix mask
   const uint2* words;
 };
@@ -106,23 +106,36 @@ __device__ __forceinline__ MaskedUnit masked_unit(const MaskedParams& p, int u) 
     w.j0 = min(n, share * per);
     w.j1 = min(n, w.j0 + per);
   }
+  // With a distance bias the walk starts at the last row's own position, where its scores are largest, and
+  // goes outwards; otherwise it starts at the end, where the masks of a causal or ragged unit lie.  Either way the
+  // first tile, which takes the exact path anyhow, settles the running maximum.
+  w.jc = w.j1 - 1;
+  if (p.slopes != nullptr) w.jc = min(max((w.start + hi) / kMaskedTile, w.j0), w.j1 - 1);
   w.words = p.words
                 ? p.words + (static_cast<size_t>(w.b) * p.n_blk + blk) * ((p.S_kv + 32 * kMaskedTile - 1) / (32 * kMaskedTile))
                 : nullptr;
   return w;
 }
 
-// Walk over a unit's KV tiles; every role of the CTA sees the same sequence.
+// Walk over a unit's KV tiles, jc down to j0 and then jc + 1 up to j1 - 1; every role of the CTA sees the same
+// sequence.
 struct MaskedTiles {
   const uint2* words;
-  int j, end, n_whole;
+  int j, j0, j1, jc, n_whole;
   int at = -1;
+  bool down = true;
   uint32_t need = 0u, whole = 0u;
   __device__ __forceinline__ explicit MaskedTiles(const MaskedUnit& w)
-      : words(w.words), j(w.j0), end(w.j1), n_whole(w.n_whole) {}
+      : words(w.words), j(w.jc), j0(w.j0), j1(w.j1), jc(w.jc), n_whole(w.n_whole) {}
   // The next tile and whether some row masks some of its keys; false at the end.
   __device__ __forceinline__ bool next(int& tile, bool& part) {
-    while (j < end) {
+    while (true) {
+      if (down ? j < j0 : j >= j1) {
+        if (!down) return false;
+        down = false;
+        j = jc + 1;
+        continue;
+      }
       part = (j + 1) * kMaskedTile > n_whole;
       if (words != nullptr) {
         if ((j >> 5) != at) {
@@ -131,19 +144,31 @@ struct MaskedTiles {
           need = x.x;
           whole = x.y;
         }
-        const uint32_t m = need >> (j & 31);
+        const uint32_t m = down ? need & (0xFFFFFFFFu >> (31 - (j & 31))) : need & (0xFFFFFFFFu << (j & 31));
         if (m == 0u) {
-          j = (at + 1) << 5;
+          j = down ? (at << 5) - 1 : (at + 1) << 5;
           continue;
         }
-        j += __ffs(m) - 1;
-        if (j >= end) return false;
+        j = (at << 5) + (down ? 31 - __clz(m) : __ffs(m) - 1);
+        if (down ? j < j0 : j >= j1) continue;
         part = (j + 1) * kMaskedTile > n_whole || !((whole >> (j & 31)) & 1u);
       }
-      tile = j++;
+      tile = j;
+      j += down ? -1 : 1;
       return true;
     }
-    return false;
+  }
+  // Tiles of the whole walk.
+  __device__ __forceinline__ int count() const {
+    if (words == nullptr || j1 <= j0) return max(j1 - j0, 0);
+    int n = 0;
+    for (int w = j0 >> 5; w * 32 < j1; ++w) {
+      uint32_t m = words[w].x;
+      if (w == j0 >> 5) m &= 0xFFFFFFFFu << (j0 & 31);
+      if (j1 - w * 32 < 32) m &= (1u << (j1 - w * 32)) - 1u;
+      n += __popc(m);
+    }
+    return n;
   }
 };
 
@@ -174,26 +199,41 @@ __global__ void __launch_bounds__(256) masked_tiles_kernel(const MaskedParams p)
   const int* kd = p.kv_doc + static_cast<size_t>(b) * p.S_kv;
   uint2* words = p.words + static_cast<size_t>(blockIdx.x) * n_words;
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.next_unit != nullptr) *p.next_unit = 0u;
-  for (int w = warp; w < n_words; w += 8) {
+  // 32 tiles at a time, four to a warp: sixteen loads of a lane in flight
+  __shared__ uint2 part[8];
+  for (int w = 0; w < n_words; ++w) {
     uint2 x = make_uint2(0u, 0u);
-    for (int t = 0; t < 32; ++t) {
-      const int k0 = (w * 32 + t) * kMaskedTile;
-      if (k0 >= p.S_kv) break;
+    int id[4][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const long long k = (w * 32LL + warp * 4 + t) * kMaskedTile + i * 32 + lane;
+        id[t][i] = k < p.S_kv ? __ldg(kd + k) : -1;
+      }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
       int klo = 0x7FFFFFFF, khi = -1, kpad = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int k = k0 + i * 32 + lane;
-        const int id = k < p.S_kv ? kd[k] : -1;
-        if (id < 0) kpad = 1;
-        else { klo = min(klo, id); khi = max(khi, id); }
+        kpad |= id[t][i] < 0;
+        klo = min(klo, id[t][i] < 0 ? 0x7FFFFFFF : id[t][i]);
+        khi = max(khi, id[t][i]);
       }
       klo = __reduce_min_sync(0xffffffffu, klo);
       khi = __reduce_max_sync(0xffffffffu, khi);
-      kpad = __reduce_max_sync(0xffffffffu, kpad);
-      if (khi >= lo && klo <= hi && hi >= 0 && khi >= 0) x.x |= 1u << t;
-      if (q_one && klo == khi && klo == lo && !kpad) x.y |= 1u << t;
+      kpad = __any_sync(0xffffffffu, kpad != 0);
+      if (khi >= lo && klo <= hi && hi >= 0 && khi >= 0) x.x |= 1u << (warp * 4 + t);
+      if (q_one && klo == khi && klo == lo && !kpad) x.y |= 1u << (warp * 4 + t);
     }
-    if (lane == 0) words[w] = x;
+    if (lane == 0) part[warp] = x;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int i = 1; i < 8; ++i) { x.x |= part[i].x; x.y |= part[i].y; }
+      words[w] = x;
+    }
+    __syncthreads();
   }
 }
 
@@ -210,7 +250,9 @@ struct MaskedCfg {
   static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsCtl <= kThreads * kRegsLaunch, "register split");
   static constexpr int kMmaWarp = 8, kTmaWarp = 9, kVWarp = 10;
   static constexpr int kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + D;
-  static constexpr float kRescaleLog2 = 8.0f, kSumBound = 256.0f;
+  // P, O and l are floating point, so a running maximum 2^40 below the true one costs no precision (dense form:
+  // 2^8): loud scores then hardly ever leave the speculative path
+  static constexpr float kRescaleLog2 = 40.0f, kSumBound = 1099511627776.0f;
   static constexpr int kOffK = kQTiles * kTileBytes;
   static constexpr int kOffV = kOffK + kStages * kTileBytes;
   static constexpr int kOffIds = kOffV + kStages * kTileBytes;      // documents of the tile's keys, per V stage
@@ -220,7 +262,7 @@ struct MaskedCfg {
   static constexpr int kUnitReaders = 1 + 2 + 8;                    // MMA, V and softmax warps
   static constexpr int kNumBars = 2 + 5 * kStages + 6 + 1 + 2 * kUnitSlots;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
-  static constexpr int kSmemBytes = kOffMisc + 16 + 4 * kUnitSlots + 1024;
+  static constexpr int kSmemBytes = kOffMisc + 16 + 8 * kUnitSlots + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
@@ -241,12 +283,13 @@ __device__ __forceinline__ float tanh_any(float x) {
   return 1.0f - __fdividef(2.0f, 1.0f + ex2_approx(x * 2.8853900817779268f));
 }
 
-// Scores s -> tanh(s * c), in place (the caller's unit becomes the cap).  The polynomial where every
+// N scores s -> tanh(s * c), in place (the caller's unit becomes the cap).  The polynomial where every
 // |s * c| <= 1 in the warp, the usual case: capping is meant for rare large scores.
-__device__ __forceinline__ void cap_scores(uint32_t (&s)[128], float c) {
+template <int N>
+__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], float c) {
   float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int i = 0; i < 128; i += 8)
+  for (int i = 0; i < N; i += 8)
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       m[k] = fmax3(m[k], fabsf(__uint_as_float(s[i + 2 * k])), fabsf(__uint_as_float(s[i + 2 * k + 1])));
@@ -254,7 +297,7 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[128], float c) {
   if (!__any_sync(0xffffffffu, far)) {
     const uint64_t c2 = f2_pack(c, c);
 #pragma unroll
-    for (int i = 0; i < 128; i += 2) {
+    for (int i = 0; i < N; i += 2) {
       float a, b;
       f2_unpack(tanh_poly2(f2_mul(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2)), a, b);
       s[i] = __float_as_uint(a);
@@ -262,32 +305,13 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[128], float c) {
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 128; ++i) s[i] = __float_as_uint(tanh_any(__uint_as_float(s[i]) * c));
+    for (int i = 0; i < N; ++i) s[i] = __float_as_uint(tanh_any(__uint_as_float(s[i]) * c));
   }
 }
 
-// Distance bias of one row in the scores' unit: s[c] - slope * |d - c|, d = position - first key of the
-// tile.  Where every row of the warp lies on one side of the tile the bias is linear in c: one
-// multiply-add each, and the part that does not depend on c is returned for the caller to add.
-__device__ __forceinline__ float bias_scores(uint32_t (&s)[128], float slope, int d, bool counts) {
-  const float df = static_cast<float>(d);
-  if (__all_sync(0xffffffffu, !counts || d >= 127)) {
-#pragma unroll
-    for (int c = 0; c < 128; ++c) s[c] = __float_as_uint(fmaf(slope, static_cast<float>(c), __uint_as_float(s[c])));
-    return -slope * df;
-  }
-  if (__all_sync(0xffffffffu, !counts || d <= 0)) {
-#pragma unroll
-    for (int c = 0; c < 128; ++c) s[c] = __float_as_uint(fmaf(-slope, static_cast<float>(c), __uint_as_float(s[c])));
-    return slope * df;
-  }
-#pragma unroll
-  for (int c = 0; c < 128; ++c)
-    s[c] = __float_as_uint(fmaf(-slope, fabsf(df - static_cast<float>(c)), __uint_as_float(s[c])));
-  return 0.0f;
-}
-
-template <int D, bool SPLIT>
+// MOD: what is done to the scores, fixed at compile time because the softmax's registers are full: 0 nothing,
+// 1 the cap, 2 the distance bias and, where given, the cap.
+template <int D, bool SPLIT, int MOD>
 __global__ void __launch_bounds__(384, 1)
     attn_masked_kernel(const __grid_constant__ MapSet<1> maps, const MaskedParams p) {
   using C = MaskedCfg<D, SPLIT>;
@@ -310,7 +334,7 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* bar_u_empty = bar_u_full + C::kUnitSlots; // [kUnitSlots]
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-  volatile int* units = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);
+  volatile int* units = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);   // [slot] {unit, tiles}
   int* ids = reinterpret_cast<int*>(smem + C::kOffIds);
   uint32_t* bad = reinterpret_cast<uint32_t*>(smem + C::kOffBad);
   uint8_t* sQ = smem;
@@ -357,11 +381,12 @@ __global__ void __launch_bounds__(384, 1)
   auto q_tiles = [&](const MaskedUnit& w) { return SPLIT ? 1 : (p.rows - w.r0 > 128 ? 2 : 1); };
 
   // The i-th unit of this CTA, as the TMA thread passed it on (n_units or more: no further one); < 0: gave up.
-  // Every reading warp frees the slot once.
+  // Every reading warp frees the slot once.  (The MMA thread takes the number of tiles along with it, because its
+  // registers, 72 less the descriptors of every K step, have no room for the walk.)
   auto unit_of = [&](int i) {
     const int slot = i % C::kUnitSlots;
     if (!mbar_wait(bar_u_full + slot, (i / C::kUnitSlots) & 1, abort_flag, tmo, 0x2D)) return -1;
-    return units[slot];
+    return units[2 * slot];
   };
   auto unit_taken = [&](int i) { mbar_arrive(bar_u_empty + i % C::kUnitSlots); };
 
@@ -380,12 +405,14 @@ __global__ void __launch_bounds__(384, 1)
           const int slot = i % C::kUnitSlots;
           if (i >= C::kUnitSlots && !(ok = mbar_wait(bar_u_empty + slot, ((i / C::kUnitSlots) + 1) & 1, abort_flag, tmo, 0x2E)))
             break;
-          units[slot] = u;
-          mbar_arrive(bar_u_full + slot);
-          if (u >= p.n_units) break;
-          const MaskedUnit w = masked_unit<SPLIT>(p, u);
-          u = p.next_unit ? static_cast<int>(gridDim.x + atomicAdd(p.next_unit, 1u)) : u + static_cast<int>(gridDim.x);
+          const bool last = u >= p.n_units;
+          const MaskedUnit w = masked_unit<SPLIT>(p, last ? 0 : u);
           MaskedTiles it(w);
+          units[2 * slot] = u;
+          units[2 * slot + 1] = it.count();
+          mbar_arrive(bar_u_full + slot);
+          if (last) break;
+          u = p.next_unit ? static_cast<int>(gridDim.x + atomicAdd(p.next_unit, 1u)) : u + static_cast<int>(gridDim.x);
           int j;
           bool part, first = true;
           while (ok && it.next(j, part)) {
@@ -465,13 +492,11 @@ __global__ void __launch_bounds__(384, 1)
         for (int i = 0; ok; ++i) {
           const int u = unit_of(i);
           if (u < 0 || u >= p.n_units) break;
+          const int tiles = units[2 * (i % C::kUnitSlots) + 1];
           unit_taken(i);
-          const MaskedUnit w = masked_unit<SPLIT>(p, u);
-          MaskedTiles it(w);
-          const int nt = q_tiles(w);
-          int j, n = 0;                          // tiles of this unit so far
-          bool part;
-          while (it.next(j, part)) {
+          const int nt = SPLIT || p.rows - (p.n_blk - 1 - u / p.runs) * 256 <= 128 ? 1 : 2;
+          int n = 0;                             // tiles of this unit so far
+          while (n < tiles) {
             if (n == 0) {
               if (!(ok = mbar_wait(bar_q_full, nq & 1, abort_flag, tmo, 0x26))) break;
               ++nq;
@@ -617,7 +642,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t tO = tmem_base + lane_off + (t ? C::kColO1 : C::kColO0);
     // one unit of the scores that the softmax sees, in natural-log and in log2 units: raw q.k, or
     // tanh(q.k * scale / cap)
-    const bool capped = p.cap > 0.0f;
+    const bool capped = MOD == 1 || (MOD == 2 && p.cap > 0.0f);
     const float unit = capped ? p.cap : p.scale;
     const float cl = unit * 1.4426950408889634f;
     const float cap_c = capped ? p.scale / p.cap : 0.0f;
@@ -645,13 +670,13 @@ __global__ void __launch_bounds__(384, 1)
           doc = __ldg(p.q_doc + static_cast<size_t>(w.b) * p.S_q + token);
           if (doc < 0) lim = 0;
         }
-        if (p.slopes != nullptr) slope = __ldg(p.slopes + head) / unit;
+        if (MOD == 2 && p.slopes != nullptr) slope = __ldg(p.slopes + head) / unit;
       }
-      float m_use = -INFINITY, l = 0.0f;
-      bool poison = false;
+      float m_use = valid_row ? -INFINITY : 0.0f, l = 0.0f;      // (rows past the end ride along with zero scores)
+      bool poison = false, started = false;       // started: every row of the warp has seen a key
       int n = 0, own = 0, j;                     // tiles of the unit, and of this stream
       bool part;
-      while (it.next(j, part)) {
+      while (__any_sync(0xffffffffu, it.next(j, part))) {
         const int st = g % NS, gp = (g / NS) & 1;
         ++g;
         ++n;
@@ -660,58 +685,96 @@ __global__ void __launch_bounds__(384, 1)
         if (!ok) break;
         ++ns;
         tc_fence_after();
+        const bool masked = __any_sync(0xffffffffu, part);   // (votes: the compiler then knows the branches uniform)
         if (warp_rows) {
           uint32_t pw[64];
           float sum = 0.0f, alpha = 1.0f;
           bool need = false;
+          // Distance bias, -slope |d - c| at column c with d = position - first key.  Where every row of the warp lies
+          // on one side of the tile it is linear in c: a multiply-add with `tilt`, and the rest, `off`, is one
+          // number for the row.
+          const int d = pos - j * kMaskedTile;
+          float tilt = 0.0f, off = 0.0f;
+          bool edit = masked;                    // scores rewritten in TMEM first (see below)
+          if (MOD == 2) {
+            const bool left = __all_sync(0xffffffffu, !valid_row || d >= 127);
+            const bool right = __all_sync(0xffffffffu, !valid_row || d <= 0);
+            if (!left && !right) edit = true;
+            tilt = left ? slope : -slope;
+            if (!edit) off = -tilt * static_cast<float>(d);
+          }
+          if (edit) {
+            // Masked tiles, and those that lie on both sides of a row: cap, bias and masks in passes of 32 columns,
+            // written back over S.  The rest of the loop then sees plain scores, and its registers, which hold
+            // a whole row of S, are spared the masks' state.
+            if (masked) {
+              ok = __all_sync(0xffffffffu, mbar_wait(bar_v_clean + st, gp, abort_flag, tmo, 0x2A));
+              if (!ok) break;
+            }
+            const int valid = masked ? lim - j * kMaskedTile : kMaskedTile;
+            const bool docs = masked && p.words != nullptr;
+#pragma unroll 1
+            for (int c0 = 0; c0 < kMaskedTile; c0 += 32) {
+              uint32_t x[32];
+              tmem_ld32_sync(tS + c0, x);
+              if (capped) cap_scores(x, cap_c);
+              if (MOD == 2) {
+                const float df = static_cast<float>(d - c0);
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  x[c] = __float_as_uint(fmaf(-slope, fabsf(df - static_cast<float>(c)), __uint_as_float(x[c])));
+              }
+              if (docs) {
+                const int4* idp = reinterpret_cast<const int4*>(ids + st * 128 + c0);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  const int4 id = idp[c];
+                  if (id.x != doc) x[4 * c] = 0xFF800000u;
+                  if (id.y != doc) x[4 * c + 1] = 0xFF800000u;
+                  if (id.z != doc) x[4 * c + 2] = 0xFF800000u;
+                  if (id.w != doc) x[4 * c + 3] = 0xFF800000u;
+                }
+              }
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (c >= valid - c0) x[c] = 0xFF800000u;
+              if (masked) {
+                for (uint32_t m = bad[st * 4 + (c0 >> 5)]; m != 0u; m &= m - 1u) {
+                  const int c = c0 + __ffs(m) - 1;
+                  poison |= c < valid && (!docs || ids[st * 128 + c] == doc);
+                }
+              }
+              tmem_st32(tS + c0, x);
+            }
+            tmem_st_wait();
+          }
           uint32_t s[128];
-          float off = 0.0f;                      // added to every score of the row
           auto scores = [&] {
             tmem_ld128_sync(tS, s);
-            if (capped) cap_scores(s, cap_c);
-            if (p.slopes != nullptr) off = bias_scores(s, slope, pos - j * kMaskedTile, valid_row);
+            if (MOD != 0 && !edit) {
+              if (capped) cap_scores(s, cap_c);
+              if (MOD == 2) {
+#pragma unroll
+                for (int c = 0; c < 128; ++c) s[c] = __float_as_uint(fmaf(tilt, static_cast<float>(c), __uint_as_float(s[c])));
+              }
+            }
           };
           scores();
-          bool slow = part || __any_sync(0xffffffffu, valid_row && m_use == -INFINITY);
+          bool slow = masked || !started;
           if (!slow) {
             // speculative pass, as in the dense form: the running maximum, kept when the row sums stay bounded
             exp_pass<false, 0>(s, cl, (m_use - off) * cl, pw, sum);
-            slow = __any_sync(0xffffffffu, valid_row && !(sum <= C::kSumBound));
+            slow = __any_sync(0xffffffffu, !(sum <= C::kSumBound));
             if (slow) scores();
           }
           if (slow) {
-            if (part) {
-              ok = __all_sync(0xffffffffu, mbar_wait(bar_v_clean + st, gp, abort_flag, tmo, 0x2A));
-              if (!ok) break;
-              const int valid = lim - j * kMaskedTile;
-              const int4* idp = reinterpret_cast<const int4*>(ids + st * 128);
-              if (w.words != nullptr) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                  const int4 x = idp[c];
-                  if (x.x != doc) s[4 * c] = 0xFF800000u;
-                  if (x.y != doc) s[4 * c + 1] = 0xFF800000u;
-                  if (x.z != doc) s[4 * c + 2] = 0xFF800000u;
-                  if (x.w != doc) s[4 * c + 3] = 0xFF800000u;
-                }
-              }
-              if (__any_sync(0xffffffffu, valid < kMaskedTile)) mask_tail(s, valid);
-              const uint4 bw = *reinterpret_cast<const uint4*>(bad + st * 4);
-              if (bw.x | bw.y | bw.z | bw.w) {
-                const uint32_t bits[4] = {bw.x, bw.y, bw.z, bw.w};
-                for (int q = 0; q < 4; ++q)
-                  for (uint32_t m = bits[q]; m != 0u; m &= m - 1u) {
-                    const int c = q * 32 + __ffs(m) - 1;
-                    poison |= c < valid && (w.words == nullptr || ids[st * 128 + c] == doc);
-                  }
-              }
-            }
             const float m_new = fmaxf(m_use, row_max128(s) + off);
             need = (m_new - m_use) * cl > C::kRescaleLog2;     // true on a row's first visible tile
             if (need) {
               alpha = ex2_approx((m_use - m_new) * cl);        // 0 when m_use = -inf
               m_use = m_new;
             }
+            started = __all_sync(0xffffffffu, m_use != -INFINITY);
             // (a row that has seen no key yet keeps m_use = -inf: exponents of -inf, p = 0)
             exp_pass<false, 0>(s, cl, m_use == -INFINITY ? 0.0f : (m_use - off) * cl, pw, sum);
           }

@@ -452,7 +452,7 @@ MaskedPlan masked_plan(int B, int H, int H_kv, int S_q, int S_kv, int D, bool do
   return m;
 }
 
-template <int D, bool SPLIT>
+template <int D, bool SPLIT, int MOD>
 int launch_masked(const void* q, const void* k, const void* v, const MaskedParams& prm, cudaStream_t st) {
   using C = MaskedCfg<D, SPLIT>;
   // the register split waits forever unless the block is launched with what it adds up to
@@ -460,13 +460,13 @@ int launch_masked(const void* q, const void* k, const void* v, const MaskedParam
   int state = split_state.load();
   if (state == 0) {
     cudaFuncAttributes attr;
-    if (cudaFuncGetAttributes(&attr, attn_masked_kernel<D, SPLIT>) != cudaSuccess) return DIT_ERR_CUDA;
+    if (cudaFuncGetAttributes(&attr, attn_masked_kernel<D, SPLIT, MOD>) != cudaSuccess) return DIT_ERR_CUDA;
     state = attr.numRegs == C::kRegsLaunch ? 1 : 2;
     split_state.store(state);
   }
   if (state != 1) return DIT_ERR_UNSUPPORTED;
   static std::atomic<uint64_t> attr_done{0};
-  int rc = ensure_smem_attr(attn_masked_kernel<D, SPLIT>, C::kSmemBytes, attr_done);
+  int rc = ensure_smem_attr(attn_masked_kernel<D, SPLIT, MOD>, C::kSmemBytes, attr_done);
   if (rc != DIT_OK) return rc;
   MapSet<1> maps;
   std::memset(&maps, 0, sizeof(maps));
@@ -487,7 +487,7 @@ int launch_masked(const void* q, const void* k, const void* v, const MaskedParam
   } else if (pr.next_unit != nullptr) {
     if (cudaMemsetAsync(pr.next_unit, 0, sizeof(unsigned int), st) != cudaSuccess) return DIT_ERR_CUDA;
   }
-  attn_masked_kernel<D, SPLIT><<<grid, C::kThreads, C::kSmemBytes, st>>>(maps, pr);
+  attn_masked_kernel<D, SPLIT, MOD><<<grid, C::kThreads, C::kSmemBytes, st>>>(maps, pr);
   if (cudaGetLastError() != cudaSuccess) return DIT_ERR_CUDA;
   if (SPLIT) {
     const long long n = static_cast<long long>(prm.runs) * prm.rows;
@@ -1171,8 +1171,13 @@ int dit_attn_fwd_masked(const void* q, const void* k, const void* v, void* out, 
   prm.part_o = reinterpret_cast<float*>(ws + plan.words_bytes);
   prm.part_lse = reinterpret_cast<float*>(ws + plan.words_bytes + plan.part_o_bytes);
   prm.timeout_ns = g_timeout_ns.load();
-  if (plan.split) return D == 64 ? launch_masked<64, true>(q, k, v, prm, st) : launch_masked<128, true>(q, k, v, prm, st);
-  return D == 64 ? launch_masked<64, false>(q, k, v, prm, st) : launch_masked<128, false>(q, k, v, prm, st);
+  if (plan.split)
+    return D == 64 ? launch_masked<64, true, 2>(q, k, v, prm, st) : launch_masked<128, true, 2>(q, k, v, prm, st);
+  if (slopes != nullptr)
+    return D == 64 ? launch_masked<64, false, 2>(q, k, v, prm, st) : launch_masked<128, false, 2>(q, k, v, prm, st);
+  if (softcap > 0.0f)
+    return D == 64 ? launch_masked<64, false, 1>(q, k, v, prm, st) : launch_masked<128, false, 1>(q, k, v, prm, st);
+  return D == 64 ? launch_masked<64, false, 0>(q, k, v, prm, st) : launch_masked<128, false, 0>(q, k, v, prm, st);
 }
 
 int dit_device_status(int* status, int clear) {
