@@ -14,19 +14,21 @@
 //   * The query heads of a key / value head lie next to each other in memory, so they make one run
 //     of query rows cut into tiles of 128 without regard to heads, which fills the tiles of few
 //     queries; where a head's rows fill its tiles well enough, each head is a run of its own.
-//   * Units differ in length, so a CTA takes its next one from a counter when it gets there (the TMA
-//     thread fetches it early and passes it on through shared memory), the longest first.
-//   * Every role walks the same list of KV tiles of its unit: the tiles up to the last key that
-//     a row of the unit may see, without those that hold no document of its rows (bits that a
-//     small kernel writes before).  Tiles that every row sees whole take the dense path (the
-//     speculative softmax); the others are masked per row and take the exact maximum first.
-//   * Long form: a unit is 256 rows as two Q tiles that share each K and V tile.
+//   * Long form: a unit is 256 rows as two Q tiles that share each K and V tile.  Units differ in
+//     length, so a CTA takes its next one from a counter when it gets there, the longest first.
 //   * Split form, for few rows against many keys: a unit is one 128-row Q tile and a share of its
 //     KV tiles; the two streams take alternate tiles, each with its own running maximum, sum
 //     and O, and the partial results (fp32) are joined by their LSEs in a second kernel.
-//   * The two idle warps of the dense form look through the V rows of masked tiles: a non-finite
-//     value would reach every row of the tile (0 * inf), so it is zeroed in shared memory and
-//     its key flagged; the rows that may see that key become NaN, the others never notice.
+//   * The TMA thread walks over the KV tiles of its unit, leaves out those that no row sees (past the last
+//     visible key; without a document of the rows, by bits that a small kernel writes before), and passes a
+//     note on each through shared memory to the other roles: per Q tile, whether it sees none of the
+//     tile (then that stream skips it), some of it, or all.
+//   * Tiles that some row sees in part come first.  They take one loop of the softmax, which rewrites S in
+//     TMEM (cap, bias, -inf) and takes the exact maximum; the whole tiles take another, the dense form's
+//     speculative one, whose registers are then free of the masks' state.
+//   * The two idle warps of the dense form look through the V rows of tiles that are masked for some row: a
+//     non-finite value would reach every row of the tile (0 * inf), so it is zeroed in shared memory
+//     and its key flagged; the rows that may see that key become NaN, the others never notice.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -53,7 +55,7 @@ struct MaskedParams {
   int n_split;                      // split form: shares of the KV tiles
   int n_units;
   unsigned int* next_unit;          // units handed out beyond the first of every CTA (zero at launch); null: in steps
-  uint2* words;                     // [B, n_blk, ceil(S_kv / 4096)] {needed, whole} tile bits, or null
+  uint4* words;                     // [B, n_blk, ceil(S_kv / 4096)] {seen, whole} tile bits of Q tiles 0 and 1, or null
   float* part_o;                    // split form: [2 n_split, B * H * S_q, D]
   float* part_lse;                  // split form: [2 n_split, B * H * S_q]
   unsigned long long timeout_ns;
@@ -61,129 +63,172 @@ struct MaskedParams {
 
 constexpr int kMaskedTile = 128;    // keys of a KV tile
 
-// What one unit computes: query rows r0.. of a run, KV tiles [j0, j1) of key head kv = b * H_kv + key head.
-struct MaskedUnit {
-  int run, kv, b, r0, start, pre;
-  int j0, j1, jc;                   // jc: where the walk starts
-  int n_whole;                      // keys [0, n_whole) are left by every row's causal / prefix mask
-  const uint2* words;
-};
-
 // First key past those that a query at this position may see (documents aside).
 __device__ __forceinline__ int masked_limit(const MaskedParams& p, int pos, int pre) {
   return p.causal ? min(max(max(pos + 1, pre), 0), p.S_kv) : p.S_kv;
 }
 
+// Query rows r0.. of run `run`, of sequence b; its share of the KV tiles (split form).
+struct MaskedUnit {
+  int run, b, r0, blk, share;
+};
+
 template <bool SPLIT>
 __device__ __forceinline__ MaskedUnit masked_unit(const MaskedParams& p, int u) {
-  constexpr int kRows = SPLIT ? 128 : 256;
   MaskedUnit w;
-  int blk, share = 0;
   if constexpr (SPLIT) {
-    share = u % p.n_split;
-    blk = (u / p.n_split) % p.n_blk;
+    w.share = u % p.n_split;
+    w.blk = (u / p.n_split) % p.n_blk;
     w.run = u / p.n_split / p.n_blk;
+    w.r0 = w.blk * 128;
   } else {
-    // the last rows (of a causal mask: the longest lists) of every run first
-    blk = p.n_blk - 1 - u / p.runs;
+    // the last rows (of a causal mask: the longest walks) of every run first
+    w.share = 0;
+    w.blk = p.n_blk - 1 - u / p.runs;
     w.run = u % p.runs;
+    w.r0 = w.blk * 256;
   }
-  const int per_b = p.H / p.run_heads;
-  w.b = w.run / per_b;
-  w.kv = w.b * p.H_kv + (w.run % per_b) * p.run_heads / (p.H / p.H_kv);
-  w.r0 = blk * kRows;
-  w.start = p.q_start ? __ldg(p.q_start + w.b) : p.S_kv - p.S_q;
-  w.pre = p.prefix ? __ldg(p.prefix + w.b) : 0;
-  const int last = min(w.r0 + kRows, p.rows) - 1;
-  const bool one_head = w.r0 / p.S_q == last / p.S_q;
-  const int lo = one_head ? w.r0 % p.S_q : 0, hi = one_head ? last % p.S_q : p.S_q - 1;
-  w.n_whole = masked_limit(p, w.start + lo, w.pre);
-  const int n = (masked_limit(p, w.start + hi, w.pre) + kMaskedTile - 1) / kMaskedTile;
-  w.j0 = 0;
-  w.j1 = n;
-  if constexpr (SPLIT) {
-    const int per = (n + p.n_split - 1) / p.n_split;
-    w.j0 = min(n, share * per);
-    w.j1 = min(n, w.j0 + per);
-  }
-  // With a distance bias the walk starts at the last row's own position, where its scores are largest, and
-  // goes outwards; otherwise it starts at the end, where the masks of a causal or ragged unit lie.  Either way the
-  // first tile, which takes the exact path anyhow, settles the running maximum.
-  w.jc = w.j1 - 1;
-  if (p.slopes != nullptr) w.jc = min(max((w.start + hi) / kMaskedTile, w.j0), w.j1 - 1);
-  w.words = p.words
-                ? p.words + (static_cast<size_t>(w.b) * p.n_blk + blk) * ((p.S_kv + 32 * kMaskedTile - 1) / (32 * kMaskedTile))
-                : nullptr;
+  w.b = w.run / (p.H / p.run_heads);
   return w;
 }
 
-// Walk over a unit's KV tiles, jc down to j0 and then jc + 1 up to j1 - 1; every role of the CTA sees the same
-// sequence.
-struct MaskedTiles {
-  const uint2* words;
-  int j, j0, j1, jc, n_whole;
-  int at = -1;
-  bool down = true;
-  uint32_t need = 0u, whole = 0u;
-  __device__ __forceinline__ explicit MaskedTiles(const MaskedUnit& w)
-      : words(w.words), j(w.jc), j0(w.j0), j1(w.j1), jc(w.jc), n_whole(w.n_whole) {}
-  // The next tile and whether some row masks some of its keys; false at the end.
-  __device__ __forceinline__ bool next(int& tile, bool& part) {
+// A note on one KV tile of a unit, from the TMA thread to the other roles.  Low bits: the tile; 3 bits for each Q
+// tile (the split form: both the same); then what the entry is.
+constexpr int kNoteTile = (1 << 23) - 1;           // S_kv <= 2^30
+constexpr int kNoteNone = 1, kNoteRange = 2, kNoteDocs = 4;   // sees nothing; some keys past a row's limit; ids to compare
+constexpr int kNoteShift = 23;                     // Q tile t's bits at kNoteShift + 3 t
+constexpr int kNoteWhole = 1 << 29;                // (a whole tile: no row masks a key, and it lies to one side of every row)
+constexpr int kNoteLast = 1 << 30;                 // the unit's last tile
+constexpr int kNoteEmpty = static_cast<int>(1u << 31);   // no tile: a unit whose rows see nothing, or (unit < 0) the end
+
+__device__ __forceinline__ int note_class(int note, int t) { return (note >> (kNoteShift + 3 * t)) & 7; }
+constexpr int kNoteMasked = 63 << kNoteShift;      // set where some row of the unit masks some key
+
+// The TMA thread's walk.  Ranges of tiles without a document mask: [js, je) lie on both sides of some row (distance
+// bias only), [jw, j1) hold a key past some row's limit, the others are whole.  Order: the first two kinds, then
+// (documents) the other tiles that a row sees in part, then the whole ones, downwards below js and upwards above
+// je.  So with a bias it goes outwards from the rows' own positions, where the scores are largest, and the first
+// tile, which takes the exact path anyhow, settles the running maximum.
+template <bool SPLIT>
+struct MaskedWalk {
+  const uint4* words;
+  int j0, j1, js, je, jw;
+  int end[2], whole[2];              // of each Q tile: first key that no row sees, first key that some row does not see
+  int seg, j, stop;
+  bool up;
+  int at;
+  uint4 x;
+
+  __device__ __forceinline__ MaskedWalk(const MaskedParams& p, const MaskedUnit& w) {
+    const int start = p.q_start ? __ldg(p.q_start + w.b) : p.S_kv - p.S_q;
+    const int pre = p.prefix ? __ldg(p.prefix + w.b) : 0;
+    int lo[2], hi[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int r = w.r0 + (SPLIT ? 0 : t * 128), last = min(r + 128, p.rows) - 1;
+      end[t] = whole[t] = 0;
+      lo[t] = hi[t] = 0;
+      if (r >= p.rows) continue;     // no rows: sees nothing
+      const bool one_head = r / p.S_q == last / p.S_q;
+      lo[t] = start + (one_head ? r % p.S_q : 0);
+      hi[t] = start + (one_head ? last % p.S_q : p.S_q - 1);
+      end[t] = masked_limit(p, hi[t], pre);
+      whole[t] = masked_limit(p, lo[t], pre);
+    }
+    const bool two = !SPLIT && p.rows - w.r0 > 128;
+    const int n = (max(end[0], end[1]) + kMaskedTile - 1) / kMaskedTile;
+    j0 = 0;
+    j1 = n;
+    if constexpr (SPLIT) {
+      const int per = (n + p.n_split - 1) / p.n_split;
+      j0 = min(n, w.share * per);
+      j1 = min(n, j0 + per);
+    }
+    jw = min(max((two ? min(whole[0], whole[1]) : whole[0]) / kMaskedTile, j0), j1);
+    js = je = jw;
+    if (p.slopes != nullptr) {
+      const int a = two ? min(lo[0], lo[1]) : lo[0], b = two ? max(hi[0], hi[1]) : hi[0];
+      js = min(max(a >= 0 ? a / kMaskedTile : 0, j0), j1);
+      je = min(max(b >= 0 ? b / kMaskedTile + 1 : 0, js), j1);
+      js = min(js, jw);
+      jw = max(jw, je);
+    }
+    words = p.words ? p.words + (static_cast<size_t>(w.b) * p.n_blk + w.blk) *
+                                    ((p.S_kv + 32 * kMaskedTile - 1) / (32 * kMaskedTile))
+                    : nullptr;
+    at = -1;
+    seg = -1;
+    j = 0;
+    stop = 1;
+    up = false;
+  }
+
+  // Segments: 0 [js, je) down, 1 [jw, j1) down; documents: 2 [j0, js) down and 3 [je, jw) up in part; 4, 5 the same, whole.
+  __device__ __forceinline__ bool next(int& note) {
     while (true) {
-      if (down ? j < j0 : j >= j1) {
-        if (!down) return false;
-        down = false;
-        j = jc + 1;
+      if (up ? j >= stop : j < stop) {
+        if (++seg == 2 && words == nullptr) seg = 4;
+        if (seg > 5) return false;
+        up = seg & 1 && seg > 1;
+        if (seg == 0) { j = je - 1; stop = js; }
+        else if (seg == 1) { j = j1 - 1; stop = jw; }
+        else if (up) { j = je; stop = jw; }
+        else { j = js - 1; stop = j0; }
         continue;
       }
-      part = (j + 1) * kMaskedTile > n_whole;
       if (words != nullptr) {
         if ((j >> 5) != at) {
           at = j >> 5;
-          const uint2 x = words[at];
-          need = x.x;
-          whole = x.y;
+          x = words[at];
         }
-        const uint32_t m = down ? need & (0xFFFFFFFFu >> (31 - (j & 31))) : need & (0xFFFFFFFFu << (j & 31));
+        uint32_t m = x.x | x.z;
+        if (seg >= 2) m &= seg < 4 ? ~(x.y & x.w) : (x.y & x.w);
+        m &= up ? 0xFFFFFFFFu << (j & 31) : 0xFFFFFFFFu >> (31 - (j & 31));
         if (m == 0u) {
-          j = down ? (at << 5) - 1 : (at + 1) << 5;
+          j = up ? (at + 1) << 5 : (at << 5) - 1;
           continue;
         }
-        j = (at << 5) + (down ? 31 - __clz(m) : __ffs(m) - 1);
-        if (down ? j < j0 : j >= j1) continue;
-        part = (j + 1) * kMaskedTile > n_whole || !((whole >> (j & 31)) & 1u);
+        j = (at << 5) + (up ? __ffs(m) - 1 : 31 - __clz(m));
+        if (up ? j >= stop : j < stop) continue;
       }
-      tile = j;
-      j += down ? -1 : 1;
+      int n = j;
+      const int bit = j & 31;
+      j += up ? 1 : -1;
+      int none = 0;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int k = n & kNoteTile;
+        int c = 0;
+        if (k * kMaskedTile >= end[t]) c = kNoteNone;
+        else if ((k + 1) * kMaskedTile > whole[t]) c = kNoteRange;
+        if (words != nullptr) {
+          const uint32_t seen = t ? x.z : x.x, all = t ? x.w : x.y;
+          if (!((seen >> bit) & 1u)) c = kNoteNone;
+          else if (!((all >> bit) & 1u) && c != kNoteNone) c |= kNoteDocs;
+        }
+        none += c == kNoteNone;
+        n |= c << (kNoteShift + 3 * t);
+      }
+      if (none == 2) continue;
+      note = n | (seg >= 4 ? kNoteWhole : 0);
       return true;
     }
   }
-  // Tiles of the whole walk.
-  __device__ __forceinline__ int count() const {
-    if (words == nullptr || j1 <= j0) return max(j1 - j0, 0);
-    int n = 0;
-    for (int w = j0 >> 5; w * 32 < j1; ++w) {
-      uint32_t m = words[w].x;
-      if (w == j0 >> 5) m &= 0xFFFFFFFFu << (j0 & 31);
-      if (j1 - w * 32 < 32) m &= (1u << (j1 - w * 32)) - 1u;
-      n += __popc(m);
-    }
-    return n;
-  }
 };
 
-// Documents: bit j of a unit's words says whether KV tile j holds a key whose document lies
-// between the smallest and largest document of the unit's rows (needed), and whether all of both
-// are one document (whole).  One CTA per (b, unit of rows); reads S_kv + 256 ids, a few KB that stay in L2.
-template <int kRows>
+// Documents: bit j of a unit's words says, for each of its Q tiles, whether KV tile j holds a key whose document
+// lies between the smallest and largest document of the Q tile's rows (seen), and whether all of both are one
+// document (whole).  One CTA per (b, unit of rows); reads S_kv + 256 ids, a few KB that stay in L2.
+template <bool SPLIT>
 __global__ void __launch_bounds__(256) masked_tiles_kernel(const MaskedParams p) {
   __shared__ int red[3][8];
+  __shared__ uint4 part[8];
   const int blk = blockIdx.x % p.n_blk, b = blockIdx.x / p.n_blk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_words = (p.S_kv + 32 * kMaskedTile - 1) / (32 * kMaskedTile);
-  const int r = blk * kRows + threadIdx.x;
+  const int r = SPLIT ? blk * 128 + static_cast<int>(threadIdx.x & 127) : blk * 256 + static_cast<int>(threadIdx.x);
   int lo = 0x7FFFFFFF, hi = -1, pad = 0;
-  if (static_cast<int>(threadIdx.x) < kRows && r < p.rows) {
+  if (r < p.rows) {
     const int id = p.q_doc[static_cast<size_t>(b) * p.S_q + r % p.S_q];
     pad = id < 0;
     if (!pad) lo = hi = id;
@@ -193,16 +238,27 @@ __global__ void __launch_bounds__(256) masked_tiles_kernel(const MaskedParams p)
   pad = __reduce_max_sync(0xffffffffu, pad);
   if (lane == 0) { red[0][warp] = lo; red[1][warp] = hi; red[2][warp] = pad; }
   __syncthreads();
+  int qlo[2], qhi[2];
+  bool one[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) { lo = min(lo, red[0][i]); hi = max(hi, red[1][i]); pad = max(pad, red[2][i]); }
-  const bool q_one = lo == hi && !pad;
+  for (int t = 0; t < 2; ++t) {
+    qlo[t] = 0x7FFFFFFF;
+    qhi[t] = -1;
+    int q_pad = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      qlo[t] = min(qlo[t], red[0][4 * t + i]);
+      qhi[t] = max(qhi[t], red[1][4 * t + i]);
+      q_pad = max(q_pad, red[2][4 * t + i]);
+    }
+    one[t] = qlo[t] == qhi[t] && !q_pad;
+  }
   const int* kd = p.kv_doc + static_cast<size_t>(b) * p.S_kv;
-  uint2* words = p.words + static_cast<size_t>(blockIdx.x) * n_words;
+  uint4* words = p.words + static_cast<size_t>(blockIdx.x) * n_words;
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.next_unit != nullptr) *p.next_unit = 0u;
   // 32 tiles at a time, four to a warp: sixteen loads of a lane in flight
-  __shared__ uint2 part[8];
   for (int w = 0; w < n_words; ++w) {
-    uint2 x = make_uint2(0u, 0u);
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
     int id[4][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -213,7 +269,8 @@ __global__ void __launch_bounds__(256) masked_tiles_kernel(const MaskedParams p)
       }
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      int klo = 0x7FFFFFFF, khi = -1, kpad = 0;
+      int klo = 0x7FFFFFFF, khi = -1;
+      bool kpad = false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         kpad |= id[t][i] < 0;
@@ -222,15 +279,18 @@ __global__ void __launch_bounds__(256) masked_tiles_kernel(const MaskedParams p)
       }
       klo = __reduce_min_sync(0xffffffffu, klo);
       khi = __reduce_max_sync(0xffffffffu, khi);
-      kpad = __any_sync(0xffffffffu, kpad != 0);
-      if (khi >= lo && klo <= hi && hi >= 0 && khi >= 0) x.x |= 1u << (warp * 4 + t);
-      if (q_one && klo == khi && klo == lo && !kpad) x.y |= 1u << (warp * 4 + t);
+      kpad = __any_sync(0xffffffffu, kpad);
+      const uint32_t bit = 1u << (warp * 4 + t);
+      if (khi >= qlo[0] && klo <= qhi[0] && qhi[0] >= 0 && khi >= 0) x.x |= bit;
+      if (one[0] && klo == khi && klo == qlo[0] && !kpad) x.y |= bit;
+      if (khi >= qlo[1] && klo <= qhi[1] && qhi[1] >= 0 && khi >= 0) x.z |= bit;
+      if (one[1] && klo == khi && klo == qlo[1] && !kpad) x.w |= bit;
     }
     if (lane == 0) part[warp] = x;
     __syncthreads();
     if (threadIdx.x == 0) {
 #pragma unroll
-      for (int i = 1; i < 8; ++i) { x.x |= part[i].x; x.y |= part[i].y; }
+      for (int i = 1; i < 8; ++i) { x.x |= part[i].x; x.y |= part[i].y; x.z |= part[i].z; x.w |= part[i].w; }
       words[w] = x;
     }
     __syncthreads();
@@ -258,11 +318,11 @@ struct MaskedCfg {
   static constexpr int kOffIds = kOffV + kStages * kTileBytes;      // documents of the tile's keys, per V stage
   static constexpr int kOffBad = kOffIds + kStages * 512;           // 128 bits of flagged keys, per V stage
   static constexpr int kOffBar = kOffBad + kStages * 16;
-  static constexpr int kUnitSlots = 4;                              // units handed on and not yet taken by every role
-  static constexpr int kUnitReaders = 1 + 2 + 8;                    // MMA, V and softmax warps
-  static constexpr int kNumBars = 2 + 5 * kStages + 6 + 1 + 2 * kUnitSlots;
+  static constexpr int kNotes = 8;                                  // notes not yet read by every role
+  static constexpr int kNoteReaders = 1 + 2 + 8;                    // MMA, V and softmax warps
+  static constexpr int kNumBars = 2 + 5 * kStages + 6 + 1 + 2 * kNotes;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
-  static constexpr int kSmemBytes = kOffMisc + 16 + 8 * kUnitSlots + 1024;
+  static constexpr int kSmemBytes = kOffMisc + 16 + 8 * kNotes + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
@@ -330,11 +390,11 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* bar_p_full = bar_s_full + 2;              // [2]
   uint64_t* bar_o_final = bar_p_full + 2;             // [2]
   uint64_t* bar_drain = bar_o_final + 2;
-  uint64_t* bar_u_full = bar_drain + 1;               // [kUnitSlots]
-  uint64_t* bar_u_empty = bar_u_full + C::kUnitSlots; // [kUnitSlots]
+  uint64_t* bar_n_full = bar_drain + 1;               // [kNotes]
+  uint64_t* bar_n_empty = bar_n_full + C::kNotes;     // [kNotes]
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-  volatile int* units = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);   // [slot] {unit, tiles}
+  volatile int2* notes = reinterpret_cast<volatile int2*>(smem + C::kOffMisc + 16);   // {note, unit}
   int* ids = reinterpret_cast<int*>(smem + C::kOffIds);
   uint32_t* bad = reinterpret_cast<uint32_t*>(smem + C::kOffBad);
   uint8_t* sQ = smem;
@@ -361,9 +421,9 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(bar_o_final + t, 1);
     }
     mbar_init(bar_drain, 1);
-    for (int s = 0; s < C::kUnitSlots; ++s) {
-      mbar_init(bar_u_full + s, 1);
-      mbar_init(bar_u_empty + s, C::kUnitReaders);
+    for (int s = 0; s < C::kNotes; ++s) {
+      mbar_init(bar_n_full + s, 1);
+      mbar_init(bar_n_empty + s, C::kNoteReaders);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -377,18 +437,13 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
-  // Q tiles of a unit that hold rows (long form; in the split form both streams use the one tile)
-  auto q_tiles = [&](const MaskedUnit& w) { return SPLIT ? 1 : (p.rows - w.r0 > 128 ? 2 : 1); };
-
-  // The i-th unit of this CTA, as the TMA thread passed it on (n_units or more: no further one); < 0: gave up.
-  // Every reading warp frees the slot once.  (The MMA thread takes the number of tiles along with it, because its
-  // registers, 72 less the descriptors of every K step, have no room for the walk.)
-  auto unit_of = [&](int i) {
-    const int slot = i % C::kUnitSlots;
-    if (!mbar_wait(bar_u_full + slot, (i / C::kUnitSlots) & 1, abort_flag, tmo, 0x2D)) return -1;
-    return units[2 * slot];
+  // The i-th note: {note, unit}.  Every reading warp frees its slot once (note_read).  Giving up reads as the end.
+  auto note_at = [&](int i) {
+    const int slot = i % C::kNotes;
+    if (!mbar_wait(bar_n_full + slot, (i / C::kNotes) & 1, abort_flag, tmo, 0x2D)) return make_int2(kNoteEmpty, -1);
+    return make_int2(notes[slot].x, notes[slot].y);
   };
-  auto unit_taken = [&](int i) { mbar_arrive(bar_u_empty + i % C::kUnitSlots); };
+  auto note_read = [&](int i) { mbar_arrive(bar_n_empty + i % C::kNotes); };
 
   if (warp >= 8) {
     regs_dec<C::kRegsCtl>();
@@ -398,50 +453,60 @@ __global__ void __launch_bounds__(384, 1)
         tma_prefetch_desc(&maps.q[0]);
         tma_prefetch_desc(&maps.k[0]);
         tma_prefetch_desc(&maps.v[0]);
-        int g = 0, nq = 0, k_issued = 0, v_issued = 0;      // running tile and Q counts
+        int g = 0, nq = 0, nn = 0, k_issued = 0, v_issued = 0;      // running tile, Q and note counts
         bool ok = true;
+        auto put = [&](int note, int u) {
+          const int slot = nn % C::kNotes;
+          if (nn >= C::kNotes && !mbar_wait(bar_n_empty + slot, ((nn / C::kNotes) + 1) & 1, abort_flag, tmo, 0x2E)) return false;
+          notes[slot].x = note;
+          notes[slot].y = u;
+          mbar_arrive(bar_n_full + slot);
+          ++nn;
+          return true;
+        };
         int u = blockIdx.x;
-        for (int i = 0; ok; ++i) {
-          const int slot = i % C::kUnitSlots;
-          if (i >= C::kUnitSlots && !(ok = mbar_wait(bar_u_empty + slot, ((i / C::kUnitSlots) + 1) & 1, abort_flag, tmo, 0x2E)))
-            break;
-          const bool last = u >= p.n_units;
-          const MaskedUnit w = masked_unit<SPLIT>(p, last ? 0 : u);
-          MaskedTiles it(w);
-          units[2 * slot] = u;
-          units[2 * slot + 1] = it.count();
-          mbar_arrive(bar_u_full + slot);
-          if (last) break;
-          u = p.next_unit ? static_cast<int>(gridDim.x + atomicAdd(p.next_unit, 1u)) : u + static_cast<int>(gridDim.x);
-          int j;
-          bool part, first = true;
-          while (ok && it.next(j, part)) {
-            if (first) {
-              first = false;
-              if (nq > 0 && !(ok = mbar_wait(bar_q_empty, (nq - 1) & 1, abort_flag, tmo, 0x20))) break;
-              const int nt = q_tiles(w);
-              mbar_arrive_expect_tx(bar_q_full, nt * C::kTileBytes);
-              for (int t = 0; t < nt; ++t)
-                for (int b = 0; b < C::kNBlk; ++b)
-                  tma_load_4d(sQ + t * C::kTileBytes + b * C::kBlkBytes, &maps.q[0], bar_q_full, b * 64,
-                              w.r0 + t * 128, w.run, 0);
-              ++nq;
-            }
+        while (ok && u < p.n_units) {
+          const MaskedUnit w = masked_unit<SPLIT>(p, u);
+          const int u_next = p.next_unit ? static_cast<int>(gridDim.x + atomicAdd(p.next_unit, 1u))
+                                         : u + static_cast<int>(gridDim.x);
+          MaskedWalk<SPLIT> walk(p, w);
+          const int kv = w.b * p.H_kv + (w.run % (p.H / p.run_heads)) * p.run_heads / (p.H / p.H_kv);
+          int note = 0, ahead = 0;
+          bool more = walk.next(ahead);
+          if (!more) {
+            ok = put(kNoteEmpty, u);
+          } else {
+            if (nq > 0 && !(ok = mbar_wait(bar_q_empty, (nq - 1) & 1, abort_flag, tmo, 0x20))) break;
+            const int nt = SPLIT || p.rows - w.r0 <= 128 ? 1 : 2;
+            mbar_arrive_expect_tx(bar_q_full, nt * C::kTileBytes);
+            for (int t = 0; t < nt; ++t)
+              for (int b = 0; b < C::kNBlk; ++b)
+                tma_load_4d(sQ + t * C::kTileBytes + b * C::kBlkBytes, &maps.q[0], bar_q_full, b * 64, w.r0 + t * 128,
+                            w.run, 0);
+            ++nq;
+          }
+          while (ok && more) {
+            note = ahead;
+            more = walk.next(ahead);
+            if (!(ok = put(note | (more ? 0 : kNoteLast), u))) break;
+            const int j = note & kNoteTile;
             const int st = g % NS;
             if (g >= NS && !(ok = mbar_wait(bar_k_empty + st, ((g / NS) + 1) & 1, abort_flag, tmo, 0x21))) break;
             mbar_arrive_expect_tx(bar_k_full + st, C::kTileBytes);
             for (int b = 0; b < C::kNBlk; ++b)
               tma_load_4d(sK + st * C::kTileBytes + b * C::kBlkBytes, &maps.k[0], bar_k_full + st, b * 64,
-                          j * kMaskedTile, w.kv, 0);
+                          j * kMaskedTile, kv, 0);
             k_issued = g + 1;
             if (g >= NS && !(ok = mbar_wait(bar_v_empty + st, ((g / NS) + 1) & 1, abort_flag, tmo, 0x22))) break;
             mbar_arrive_expect_tx(bar_v_full + st, C::kTileBytes);
             for (int b = 0; b < C::kNBlk; ++b)
               tma_load_4d(sV + st * C::kTileBytes + b * C::kBlkBytes, &maps.v[0], bar_v_full + st, b * 64,
-                          j * kMaskedTile, w.kv, 0);
+                          j * kMaskedTile, kv, 0);
             v_issued = ++g;
           }
+          u = u_next;
         }
+        if (ok) put(kNoteEmpty, -1);
         // the last load of every stage must land before the CTA may exit
         if (nq > 0) mbar_wait_drain(bar_q_full, (nq - 1) & 1, tmo);
         for (int r = 0; r < NS; ++r) {
@@ -489,18 +554,19 @@ __global__ void __launch_bounds__(384, 1)
           ++np[t];
           return r;
         };
-        for (int i = 0; ok; ++i) {
-          const int u = unit_of(i);
-          if (u < 0 || u >= p.n_units) break;
-          const int tiles = units[2 * (i % C::kUnitSlots) + 1];
-          unit_taken(i);
-          const int nt = SPLIT || p.rows - (p.n_blk - 1 - u / p.runs) * 256 <= 128 ? 1 : 2;
+        for (int i = 0; ok;) {
+          int2 e = note_at(i);
+          if (e.y < 0) break;
+          if (e.x & kNoteEmpty) {
+            note_read(i++);
+            continue;
+          }
+          if (!(ok = mbar_wait(bar_q_full, nq & 1, abort_flag, tmo, 0x26))) break;
+          ++nq;
           int n = 0;                             // tiles of this unit so far
-          while (n < tiles) {
-            if (n == 0) {
-              if (!(ok = mbar_wait(bar_q_full, nq & 1, abort_flag, tmo, 0x26))) break;
-              ++nq;
-            }
+          int prev = 0, begun = 0;               // streams that own the previous tile, that have begun their O
+          while (true) {
+            note_read(i++);
             const int st = g % NS;
             if (!(ok = mbar_wait(bar_k_full + st, (g / NS) & 1, abort_flag, tmo, 0x23))) break;
             tc_fence_after();
@@ -517,49 +583,56 @@ __global__ void __launch_bounds__(384, 1)
               tc_commit(bar_s_full + t);
             } else {
               const int vs = (g - 1 + NS) % NS;
-              if (n > 0) {
-                if (!(ok = wait_v(g - 1) && wait_p(0))) break;
-                tc_fence_after();
-                issue_pv(0, vs, n > 1);
-                if (nt == 1) tc_commit(bar_v_empty + vs);
-              }
-              issue_s(0, st);
-              tc_commit(bar_s_full + 0);
-              if (nt == 2) {
-                if (n > 0) {
-                  if (!(ok = wait_p(1))) break;
+              if (prev && !(ok = wait_v(g - 1))) break;
+              const int own = (note_class(e.x, 0) != kNoteNone ? 1 : 0) | (note_class(e.x, 1) != kNoteNone ? 2 : 0);
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                if (prev & (1 << t)) {
+                  if (!(ok = wait_p(t))) break;
                   tc_fence_after();
-                  issue_pv(1, vs, n > 1);
-                  tc_commit(bar_v_empty + vs);
+                  issue_pv(t, vs, begun & (1 << t));
+                  begun |= 1 << t;
                 }
-                issue_s(1, st);
-                tc_commit(bar_s_full + 1);
+                if (t == 1 && prev) tc_commit(bar_v_empty + vs);
+                if (own & (1 << t)) {
+                  issue_s(t, st);
+                  tc_commit(bar_s_full + t);
+                }
               }
+              if (!ok) break;
+              prev = own;
             }
             tc_commit(bar_k_empty + st);
             ++g;
             ++n;
+            if (e.x & kNoteLast) break;
+            e = note_at(i);
+            if (!(ok = e.y >= 0)) break;
           }
           if (!ok) break;
-          if (n == 0) continue;
           tc_commit(bar_q_empty);                // every S MMA of this unit is issued
           if constexpr (SPLIT) {
-            for (int e = n >= 2 ? n - 2 : 0; ok && e < n; ++e) {
-              const int t = e & 1, gt = g - n + e;
+            for (int k = n >= 2 ? n - 2 : 0; ok && k < n; ++k) {
+              const int t = k & 1, gt = g - n + k;
               if (!(ok = wait_v(gt) && wait_p(t))) break;
               tc_fence_after();
-              issue_pv(t, gt % NS, e >= 2);
+              issue_pv(t, gt % NS, k >= 2);
               tc_commit(bar_o_final + t);
               tc_commit(bar_v_empty + gt % NS);
             }
           } else {
             const int vs = (g - 1) % NS;
             ok = wait_v(g - 1);
-            for (int t = 0; ok && t < nt; ++t) {
-              if (!(ok = wait_p(t))) break;
-              tc_fence_after();
-              issue_pv(t, vs, n > 1);
-              tc_commit(bar_o_final + t);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (ok && (prev & (1 << t))) {
+                if ((ok = wait_p(t))) {
+                  tc_fence_after();
+                  issue_pv(t, vs, begun & (1 << t));
+                  begun |= 1 << t;
+                }
+              }
+              if (ok && (begun & (1 << t))) tc_commit(bar_o_final + t);
             }
             if (ok) tc_commit(bar_v_empty + vs);
           }
@@ -575,27 +648,26 @@ __global__ void __launch_bounds__(384, 1)
       bool ok = true;
       int g = 0;
       for (int i = 0; ok; ++i) {
-        const int u = unit_of(i);
+        const int2 e = note_at(i);
         __syncwarp();
-        if (__any_sync(0xffffffffu, u < 0 || u >= p.n_units)) break;
-        if (lane == 0) unit_taken(i);
-        const MaskedUnit w = masked_unit<SPLIT>(p, u);
-        MaskedTiles it(w);
-        int j;
-        bool part;
-        while (it.next(j, part)) {
+        if (__any_sync(0xffffffffu, e.y < 0)) break;
+        if (lane == 0) note_read(i);
+        if (e.x & kNoteEmpty) continue;
+        const bool part = e.x & kNoteMasked;
+        const bool docs = p.words != nullptr && ((note_class(e.x, 0) | note_class(e.x, 1)) & kNoteDocs);
+        {
           const int st = g % NS;
           int id0 = -1, id1 = -1;
-          if (part && w.words != nullptr) {
-            const int k = j * kMaskedTile + half * 64 + lane;
-            const int* kd = p.kv_doc + static_cast<size_t>(w.b) * p.S_kv;
-            if (k < p.S_kv) id0 = __ldg(kd + k);
-            if (k + 32 < p.S_kv) id1 = __ldg(kd + k + 32);
+          if (docs) {
+            const int k = (e.x & kNoteTile) * kMaskedTile + half * 64 + lane;
+            const int* kd = p.kv_doc + static_cast<size_t>(masked_unit<SPLIT>(p, e.y).b) * p.S_kv;
+            if (k < p.S_kv) id0 = max(__ldg(kd + k), -1);
+            if (k + 32 < p.S_kv) id1 = max(__ldg(kd + k + 32), -1);
           }
           ok = __all_sync(0xffffffffu, mbar_wait(bar_v_full + st, (g / NS) & 1, abort_flag, tmo, 0x27));
           if (!ok) break;
           if (part) {
-            if (w.words != nullptr) {
+            if (docs) {
               ids[st * 128 + half * 64 + lane] = id0;
               ids[st * 128 + half * 64 + 32 + lane] = id1;
             }
@@ -649,159 +721,197 @@ __global__ void __launch_bounds__(384, 1)
     bool ok = true;
     int g = 0, ns = 0, no = 0;                   // running tiles of the CTA, S tiles and O's of this stream
 
-    for (int i = 0; ok; ++i) {
-      const int u = unit_of(i);
+    for (int i = 0; ok;) {
+      int2 e = note_at(i);
       __syncwarp();
-      if (__any_sync(0xffffffffu, u < 0 || u >= p.n_units)) break;
-      if (lane == 0) unit_taken(i);
+      if (__any_sync(0xffffffffu, e.y < 0)) break;
+      const int u = e.y;
       const MaskedUnit w = masked_unit<SPLIT>(p, u);
-      MaskedTiles it(w);
-      const bool mine = SPLIT || t < q_tiles(w);
       const int r = w.r0 + (SPLIT ? 0 : t * 128) + row;
       const bool valid_row = r < p.rows;
       const bool warp_rows = __any_sync(0xffffffffu, valid_row);
-      const int token = r % p.S_q, head = w.run % (p.H / p.run_heads) * p.run_heads + r / p.S_q;
-      const int pos = w.start + token;
-      int lim = p.S_kv, doc = -1;
+      int pos, lim = p.S_kv, doc = -2;            // (-2: no key's document, padding's is -1)
       float slope = 0.0f;
-      if (valid_row) {
-        lim = masked_limit(p, pos, w.pre);
-        if (w.words != nullptr) {
-          doc = __ldg(p.q_doc + static_cast<size_t>(w.b) * p.S_q + token);
-          if (doc < 0) lim = 0;
+      {
+        const int token = r % p.S_q, head = w.run % (p.H / p.run_heads) * p.run_heads + r / p.S_q;
+        pos = (p.q_start ? __ldg(p.q_start + w.b) : p.S_kv - p.S_q) + token;
+        if (valid_row) {
+          lim = masked_limit(p, pos, p.prefix ? __ldg(p.prefix + w.b) : 0);
+          if (p.words != nullptr) {
+            doc = __ldg(p.q_doc + static_cast<size_t>(w.b) * p.S_q + token);
+            if (doc < 0) doc = -2;
+          }
+          if (MOD == 2 && p.slopes != nullptr) slope = __ldg(p.slopes + head) / unit;
         }
-        if (MOD == 2 && p.slopes != nullptr) slope = __ldg(p.slopes + head) / unit;
       }
       float m_use = valid_row ? -INFINITY : 0.0f, l = 0.0f;      // (rows past the end ride along with zero scores)
       bool poison = false, started = false;       // started: every row of the warp has seen a key
-      int n = 0, own = 0, j;                     // tiles of the unit, and of this stream
-      bool part;
-      while (__any_sync(0xffffffffu, it.next(j, part))) {
-        const int st = g % NS, gp = (g / NS) & 1;
-        ++g;
+      int n = 0, own = 0;                         // tiles of the unit, and of this stream
+
+      // One tile's S: the next of this stream, if it owns the tile.
+      auto take = [&] {
+        const bool mine = SPLIT ? (n & 1) == t : note_class(e.x, t) != kNoteNone;
         ++n;
-        if (!mine || (SPLIT && ((n - 1) & 1) != t)) continue;
+        if (!mine) return false;
         ok = __all_sync(0xffffffffu, mbar_wait(bar_s_full + t, ns & 1, abort_flag, tmo, 0x28 + t));
-        if (!ok) break;
         ++ns;
         tc_fence_after();
-        const bool masked = __any_sync(0xffffffffu, part);   // (votes: the compiler then knows the branches uniform)
-        if (warp_rows) {
-          uint32_t pw[64];
-          float sum = 0.0f, alpha = 1.0f;
-          bool need = false;
-          // Distance bias, -slope |d - c| at column c with d = position - first key.  Where every row of the warp lies
-          // on one side of the tile it is linear in c: a multiply-add with `tilt`, and the rest, `off`, is one
-          // number for the row.
-          const int d = pos - j * kMaskedTile;
-          float tilt = 0.0f, off = 0.0f;
-          bool edit = masked;                    // scores rewritten in TMEM first (see below)
-          if (MOD == 2) {
-            const bool left = __all_sync(0xffffffffu, !valid_row || d >= 127);
-            const bool right = __all_sync(0xffffffffu, !valid_row || d <= 0);
-            if (!left && !right) edit = true;
-            tilt = left ? slope : -slope;
-            if (!edit) off = -tilt * static_cast<float>(d);
-          }
-          if (edit) {
-            // Masked tiles, and those that lie on both sides of a row: cap, bias and masks in passes of 32 columns,
-            // written back over S.  The rest of the loop then sees plain scores, and its registers, which hold
-            // a whole row of S, are spared the masks' state.
-            if (masked) {
-              ok = __all_sync(0xffffffffu, mbar_wait(bar_v_clean + st, gp, abort_flag, tmo, 0x2A));
-              if (!ok) break;
-            }
-            const int valid = masked ? lim - j * kMaskedTile : kMaskedTile;
-            const bool docs = masked && p.words != nullptr;
+        return ok;
+      };
+      // P to TMEM, O to the new maximum, the row sum; then the tile is the MMA thread's.
+      auto give = [&](uint32_t (&pw)[64], float sum, float alpha, bool need) {
+        tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&pw[0]));
+        tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pw[32]));
+        tmem_st_wait();
+        // O_t is quiescent here: the P.V of this stream's previous tile completed before S was signalled
+        if (own > 0 && __any_sync(0xffffffffu, need)) {
 #pragma unroll 1
-            for (int c0 = 0; c0 < kMaskedTile; c0 += 32) {
-              uint32_t x[32];
-              tmem_ld32_sync(tS + c0, x);
-              if (capped) cap_scores(x, cap_c);
-              if (MOD == 2) {
-                const float df = static_cast<float>(d - c0);
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t o[32];
+            tmem_ld32_sync(tO + cc * 32, o);
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  x[c] = __float_as_uint(fmaf(-slope, fabsf(df - static_cast<float>(c)), __uint_as_float(x[c])));
-              }
-              if (docs) {
-                const int4* idp = reinterpret_cast<const int4*>(ids + st * 128 + c0);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                  const int4 id = idp[c];
-                  if (id.x != doc) x[4 * c] = 0xFF800000u;
-                  if (id.y != doc) x[4 * c + 1] = 0xFF800000u;
-                  if (id.z != doc) x[4 * c + 2] = 0xFF800000u;
-                  if (id.w != doc) x[4 * c + 3] = 0xFF800000u;
-                }
-              }
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (c >= valid - c0) x[c] = 0xFF800000u;
-              if (masked) {
-                for (uint32_t m = bad[st * 4 + (c0 >> 5)]; m != 0u; m &= m - 1u) {
-                  const int c = c0 + __ffs(m) - 1;
-                  poison |= c < valid && (!docs || ids[st * 128 + c] == doc);
-                }
-              }
-              tmem_st32(tS + c0, x);
-            }
-            tmem_st_wait();
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st32(tO + cc * 32, o);
           }
-          uint32_t s[128];
-          auto scores = [&] {
-            tmem_ld128_sync(tS, s);
-            if (MOD != 0 && !edit) {
-              if (capped) cap_scores(s, cap_c);
-              if (MOD == 2) {
-#pragma unroll
-                for (int c = 0; c < 128; ++c) s[c] = __float_as_uint(fmaf(tilt, static_cast<float>(c), __uint_as_float(s[c])));
-              }
-            }
-          };
-          scores();
-          bool slow = masked || !started;
-          if (!slow) {
-            // speculative pass, as in the dense form: the running maximum, kept when the row sums stay bounded
-            exp_pass<false, 0>(s, cl, (m_use - off) * cl, pw, sum);
-            slow = __any_sync(0xffffffffu, !(sum <= C::kSumBound));
-            if (slow) scores();
-          }
-          if (slow) {
-            const float m_new = fmaxf(m_use, row_max128(s) + off);
-            need = (m_new - m_use) * cl > C::kRescaleLog2;     // true on a row's first visible tile
-            if (need) {
-              alpha = ex2_approx((m_use - m_new) * cl);        // 0 when m_use = -inf
-              m_use = m_new;
-            }
-            started = __all_sync(0xffffffffu, m_use != -INFINITY);
-            // (a row that has seen no key yet keeps m_use = -inf: exponents of -inf, p = 0)
-            exp_pass<false, 0>(s, cl, m_use == -INFINITY ? 0.0f : (m_use - off) * cl, pw, sum);
-          }
-          tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&pw[0]));
-          tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pw[32]));
           tmem_st_wait();
-          // O_t is quiescent here: the P.V of this stream's previous tile completed before S was signalled
-          if (own > 0 && __any_sync(0xffffffffu, need)) {
-#pragma unroll 1
-            for (int cc = 0; cc < D / 32; ++cc) {
-              uint32_t o[32];
-              tmem_ld32_sync(tO + cc * 32, o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st32(tO + cc * 32, o);
-            }
-            tmem_st_wait();
-          }
-          l = fmaf(l, alpha, sum);
         }
+        l = fmaf(l, alpha, sum);
+      };
+      auto publish = [&] {
         ++own;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_p_full + t);
+      };
+      // The next note of this unit, false after its last.
+      auto advance = [&] {
+        ++g;
+        __syncwarp();
+        if (lane == 0) note_read(i);
+        ++i;
+        if (e.x & kNoteLast) return false;
+        e = note_at(i);
+        ok = __all_sync(0xffffffffu, e.y >= 0);
+        return ok;
+      };
+      // Distance bias of a tile to one side of the row: slope times the distance is linear in the column; a multiply-add
+      // with `tilt` for each, and the rest is one number for the row, returned.
+      auto tilt_scores = [&](uint32_t (&s)[128], int d) {
+        const float tilt = d > 0 ? slope : -slope;
+#pragma unroll
+        for (int c = 0; c < 128; ++c) s[c] = __float_as_uint(fmaf(tilt, static_cast<float>(c), __uint_as_float(s[c])));
+        return -tilt * static_cast<float>(d);
+      };
+      auto exact = [&](uint32_t (&s)[128], float off, uint32_t (&pw)[64], float& sum, float& alpha, bool& need) {
+        const float m_new = fmaxf(m_use, row_max128(s) + off);
+        need = (m_new - m_use) * cl > C::kRescaleLog2;           // true on a row's first visible tile
+        if (need) {
+          alpha = ex2_approx((m_use - m_new) * cl);              // 0 when m_use = -inf
+          m_use = m_new;
+        }
+        started = __all_sync(0xffffffffu, m_use != -INFINITY);
+        // (a row that has seen no key yet keeps m_use = -inf: exponents of -inf, p = 0)
+        exp_pass<false, 0>(s, cl, m_use == -INFINITY ? 0.0f : (m_use - off) * cl, pw, sum);
+      };
+
+      bool more = !(e.x & kNoteEmpty);
+      if (!more) {
+        __syncwarp();
+        if (lane == 0) note_read(i);
+        ++i;
+      }
+      // ---- tiles that some row of the unit sees in part, or that lie on both sides of a row
+      while (more && !__any_sync(0xffffffffu, e.x & kNoteWhole)) {
+        if (take()) {
+          if (warp_rows) {
+            const int cls = note_class(e.x, t), j = e.x & kNoteTile, st = g % NS;
+            const bool docs = cls & kNoteDocs;
+            const int valid = cls & kNoteRange ? lim - j * kMaskedTile : kMaskedTile;
+            const int d = pos - j * kMaskedTile;
+            if (e.x & kNoteMasked) {
+              ok = __all_sync(0xffffffffu, mbar_wait(bar_v_clean + st, (g / NS) & 1, abort_flag, tmo, 0x2A));
+              if (!ok) break;
+              for (int q = 0; q < 4; ++q)
+                for (uint32_t m = bad[st * 4 + q]; m != 0u; m &= m - 1u) {
+                  const int c = q * 32 + __ffs(m) - 1;
+                  poison |= c < valid && (!docs || ids[st * 128 + c] == doc);
+                }
+            }
+            // Cap, bias and masks in passes of 32 columns, written back over S.
+            if (MOD == 2 || cls != 0) {
+#pragma unroll 1
+              for (int c0 = 0; c0 < kMaskedTile; c0 += 32) {
+                uint32_t x[32];
+                tmem_ld32_sync(tS + c0, x);
+                if (capped) cap_scores(x, cap_c);
+                if (MOD == 2) {
+                  const float df = static_cast<float>(d - c0);
+#pragma unroll
+                  for (int c = 0; c < 32; ++c)
+                    x[c] = __float_as_uint(fmaf(-slope, fabsf(df - static_cast<float>(c)), __uint_as_float(x[c])));
+                }
+                if (docs) {
+                  const int4* idp = reinterpret_cast<const int4*>(ids + st * 128 + c0);
+#pragma unroll
+                  for (int c = 0; c < 8; ++c) {
+                    const int4 id = idp[c];
+                    if (id.x != doc) x[4 * c] = 0xFF800000u;
+                    if (id.y != doc) x[4 * c + 1] = 0xFF800000u;
+                    if (id.z != doc) x[4 * c + 2] = 0xFF800000u;
+                    if (id.w != doc) x[4 * c + 3] = 0xFF800000u;
+                  }
+                }
+                if (__any_sync(0xffffffffu, valid < c0 + 32)) {
+#pragma unroll
+                  for (int c = 0; c < 32; ++c)
+                    if (c >= valid - c0) x[c] = 0xFF800000u;
+                }
+                tmem_st32(tS + c0, x);
+              }
+              tmem_st_wait();
+            }
+            uint32_t s[128], pw[64];
+            float sum = 0.0f, alpha = 1.0f;
+            bool need = false;
+            tmem_ld128_sync(tS, s);
+            if (MOD == 1 && cls == 0) cap_scores(s, cap_c);
+            exact(s, 0.0f, pw, sum, alpha, need);
+            give(pw, sum, alpha, need);
+          }
+          publish();
+        }
+        if (!ok) break;
+        more = advance();
+      }
+      // ---- whole tiles
+      while (more && ok) {
+        if (take()) {
+          if (warp_rows) {
+            uint32_t s[128], pw[64];
+            float sum = 0.0f, alpha = 1.0f, off = 0.0f;
+            bool need = false;
+            auto scores = [&] {
+              tmem_ld128_sync(tS, s);
+              if (capped) cap_scores(s, cap_c);
+              if (MOD == 2) off = tilt_scores(s, pos - (e.x & kNoteTile) * kMaskedTile);
+            };
+            scores();
+            bool slow = !started;
+            if (!slow) {
+              // speculative pass, as in the dense form: the running maximum, kept when the row sums stay bounded
+              exp_pass<false, 0>(s, cl, (m_use - off) * cl, pw, sum);
+              slow = __any_sync(0xffffffffu, !(sum <= C::kSumBound));
+              if (slow) scores();
+            }
+            if (slow) exact(s, off, pw, sum, alpha, need);
+            give(pw, sum, alpha, need);
+          }
+          publish();
+        }
+        if (!ok) break;
+        more = advance();
       }
       if (!ok) break;
-      if (!mine) continue;
 
       // ---------------------------------------------------------------- epilogue
       if (own > 0) {
@@ -818,7 +928,7 @@ __global__ void __launch_bounds__(384, 1)
       const size_t row_idx = static_cast<size_t>(w.run) * p.rows + r;
       if constexpr (SPLIT) {
         const size_t n_rows = static_cast<size_t>(p.runs) * p.rows;
-        const size_t at = static_cast<size_t>(2 * (u % p.n_split) + t) * n_rows + row_idx;
+        const size_t at = static_cast<size_t>(2 * w.share + t) * n_rows + row_idx;
         if (valid_row) p.part_lse[at] = lse;
         if (own > 0)
 #pragma unroll 1

@@ -441,7 +441,7 @@ MaskedPlan masked_plan(int B, int H, int H_kv, int S_q, int S_kv, int D, bool do
   m.units = static_cast<long long>(m.runs) * m.n_blk * (m.split ? m.n_split : 1);
   auto pad = [](size_t n) { return (n + 255) / 256 * 256; };
   m.next_bytes = 256;
-  if (docs) m.words_bytes = pad(static_cast<size_t>(B) * m.n_blk * ((tiles + 31) / 32) * 8);
+  if (docs) m.words_bytes = pad(static_cast<size_t>(B) * m.n_blk * ((tiles + 31) / 32) * 16);
   if (m.split) {
     const size_t n = static_cast<size_t>(2 * m.n_split) * m.runs * m.rows;
     m.part_o_bytes = pad(n * D * 4);
@@ -482,7 +482,7 @@ int launch_masked(const void* q, const void* k, const void* v, const MaskedParam
   MaskedParams pr = prm;
   if (pr.n_units <= grid) pr.next_unit = nullptr;
   if (pr.words != nullptr) {
-    masked_tiles_kernel<SPLIT ? 128 : 256><<<pr.B * pr.n_blk, 256, 0, st>>>(pr);
+    masked_tiles_kernel<SPLIT><<<pr.B * pr.n_blk, 256, 0, st>>>(pr);
     if (cudaGetLastError() != cudaSuccess) return DIT_ERR_CUDA;
   } else if (pr.next_unit != nullptr) {
     if (cudaMemsetAsync(pr.next_unit, 0, sizeof(unsigned int), st) != cudaSuccess) return DIT_ERR_CUDA;
@@ -1167,7 +1167,7 @@ int dit_attn_fwd_masked(const void* q, const void* k, const void* v, void* out, 
   prm.run_heads = plan.run_heads; prm.runs = plan.runs;
   prm.next_unit = plan.next_bytes ? reinterpret_cast<unsigned int*>(ws) : nullptr;
   ws += plan.next_bytes;
-  prm.words = q_doc != nullptr ? reinterpret_cast<uint2*>(ws) : nullptr;
+  prm.words = q_doc != nullptr ? reinterpret_cast<uint4*>(ws) : nullptr;
   prm.part_o = reinterpret_cast<float*>(ws + plan.words_bytes);
   prm.part_lse = reinterpret_cast<float*>(ws + plan.words_bytes + plan.part_o_bytes);
   prm.timeout_ns = g_timeout_ns.load();
