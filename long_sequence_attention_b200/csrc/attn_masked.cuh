@@ -22,7 +22,7 @@
 //   * The TMA thread walks over the KV tiles of its unit, leaves out those that no row sees (past the last
 //     visible key; without a document of the rows, by bits that a small kernel writes before), and passes a
 //     note on each through shared memory to the other roles: per Q tile, whether it sees none of the
-//     tile (then that stream skips it), some of it, or all.
+//     tile (then that stream skips it), some of it, or all.  Neighbouring whole tiles share a note.
 //   * Tiles that some row sees in part come first.  They take one loop of the softmax, which rewrites S in
 //     TMEM (cap, bias, -inf) and takes the exact maximum; the whole tiles take another, the dense form's
 //     speculative one, whose registers are then free of the masks' state.
@@ -92,17 +92,17 @@ __device__ __forceinline__ MaskedUnit masked_unit(const MaskedParams& p, int u) 
   return w;
 }
 
-// A note on one KV tile of a unit, from the TMA thread to the other roles.  Low bits: the tile; 3 bits for each Q
-// tile (the split form: both the same); then what the entry is.
+// A note {x, unit, n, masked} on n KV tiles of a unit (|n| neighbours; n < 0: downwards), from the TMA thread to the
+// other roles.  masked: some row does not see some key.  x, low bits: the first tile; 3 bits for each Q tile (the
+// split form: both the same); then what the note is.
 constexpr int kNoteTile = (1 << 23) - 1;           // S_kv <= 2^30
 constexpr int kNoteNone = 1, kNoteRange = 2, kNoteDocs = 4;   // sees nothing; some keys past a row's limit; ids to compare
 constexpr int kNoteShift = 23;                     // Q tile t's bits at kNoteShift + 3 t
 constexpr int kNoteWhole = 1 << 29;                // (a whole tile: no row masks a key, and it lies to one side of every row)
-constexpr int kNoteLast = 1 << 30;                 // the unit's last tile
+constexpr int kNoteLast = 1 << 30;                 // the unit's last note
 constexpr int kNoteEmpty = static_cast<int>(1u << 31);   // no tile: a unit whose rows see nothing, or (unit < 0) the end
 
 __device__ __forceinline__ int note_class(int note, int t) { return (note >> (kNoteShift + 3 * t)) & 7; }
-constexpr int kNoteMasked = 63 << kNoteShift;      // set where some row of the unit masks some key
 
 // The TMA thread's walk.  Ranges of tiles without a document mask: [js, je) lie on both sides of some row (distance
 // bias only), [jw, j1) hold a key past some row's limit, the others are whole.  Order: the first two kinds, then
@@ -115,7 +115,7 @@ struct MaskedWalk {
   int j0, j1, js, je, jw;
   int end[2], whole[2];              // of each Q tile: first key that no row sees, first key that some row does not see
   int seg, j, stop;
-  bool up;
+  bool up, two;                      // two: rows in both Q tiles
   int at;
   uint4 x;
 
@@ -135,7 +135,7 @@ struct MaskedWalk {
       end[t] = masked_limit(p, hi[t], pre);
       whole[t] = masked_limit(p, lo[t], pre);
     }
-    const bool two = !SPLIT && p.rows - w.r0 > 128;
+    two = !SPLIT && p.rows - w.r0 > 128;
     const int n = (max(end[0], end[1]) + kMaskedTile - 1) / kMaskedTile;
     j0 = 0;
     j1 = n;
@@ -164,7 +164,7 @@ struct MaskedWalk {
   }
 
   // Segments: 0 [js, je) down, 1 [jw, j1) down; documents: 2 [j0, js) down and 3 [je, jw) up in part; 4, 5 the same, whole.
-  __device__ __forceinline__ bool next(int& note) {
+  __device__ __forceinline__ bool next(int& note, int& run, bool& masked) {
     while (true) {
       if (up ? j >= stop : j < stop) {
         if (++seg == 2 && words == nullptr) seg = 4;
@@ -193,8 +193,19 @@ struct MaskedWalk {
       }
       int n = j;
       const int bit = j & 31;
-      j += up ? 1 : -1;
+      run = up ? 1 : -1;
+      if (seg >= 4) {                // whole tiles: as many as follow one another (documents: within a word)
+        int len = up ? stop - j : j - stop + 1;
+        if (words != nullptr) {
+          const uint32_t m = ~(x.y & x.w);
+          len = min(len, up ? (m >> bit ? __ffs(m >> bit) - 1 : 32 - bit)
+                            : (m << (31 - bit) ? __clz(m << (31 - bit)) : bit + 1));
+        }
+        run = up ? len : -len;
+      }
+      j += run;
       int none = 0;
+      masked = false;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const int k = n & kNoteTile;
@@ -207,6 +218,7 @@ struct MaskedWalk {
           else if (!((all >> bit) & 1u) && c != kNoteNone) c |= kNoteDocs;
         }
         none += c == kNoteNone;
+        masked |= c != 0 && (t == 0 || SPLIT || two);
         n |= c << (kNoteShift + 3 * t);
       }
       if (none == 2) continue;
@@ -253,6 +265,7 @@ __global__ void __launch_bounds__(256) masked_tiles_kernel(const MaskedParams p)
     }
     one[t] = qlo[t] == qhi[t] && !q_pad;
   }
+  const bool absent = !SPLIT && blk * 256 + 128 >= p.rows;   // no second Q tile: it does not keep tiles from being whole
   const int* kd = p.kv_doc + static_cast<size_t>(b) * p.S_kv;
   uint4* words = p.words + static_cast<size_t>(blockIdx.x) * n_words;
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.next_unit != nullptr) *p.next_unit = 0u;
@@ -284,7 +297,7 @@ __global__ void __launch_bounds__(256) masked_tiles_kernel(const MaskedParams p)
       if (khi >= qlo[0] && klo <= qhi[0] && qhi[0] >= 0 && khi >= 0) x.x |= bit;
       if (one[0] && klo == khi && klo == qlo[0] && !kpad) x.y |= bit;
       if (khi >= qlo[1] && klo <= qhi[1] && qhi[1] >= 0 && khi >= 0) x.z |= bit;
-      if (one[1] && klo == khi && klo == qlo[1] && !kpad) x.w |= bit;
+      if (absent || (one[1] && klo == khi && klo == qlo[1] && !kpad)) x.w |= bit;
     }
     if (lane == 0) part[warp] = x;
     __syncthreads();
@@ -318,11 +331,12 @@ struct MaskedCfg {
   static constexpr int kOffIds = kOffV + kStages * kTileBytes;      // documents of the tile's keys, per V stage
   static constexpr int kOffBad = kOffIds + kStages * 512;           // 128 bits of flagged keys, per V stage
   static constexpr int kOffBar = kOffBad + kStages * 16;
-  static constexpr int kNotes = 8;                                  // notes not yet read by every role
-  static constexpr int kNoteReaders = 1 + 2 + 8;                    // MMA, V and softmax warps
-  static constexpr int kNumBars = 2 + 5 * kStages + 6 + 1 + 2 * kNotes;
+  static constexpr int kNotes = 4;                                   // notes not yet read by every role
+  static constexpr int kNoteReaders = 1 + 8;                        // MMA and softmax warps
+  static constexpr int kVNotes = 2;                                 // notes on masked tiles for the V warps
+  static constexpr int kNumBars = 2 + 5 * kStages + 6 + 1 + 2 * kNotes + 2 * kVNotes;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
-  static constexpr int kSmemBytes = kOffMisc + 16 + 8 * kNotes + 1024;
+  static constexpr int kSmemBytes = kOffMisc + 16 + 16 * (kNotes + kVNotes) + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
@@ -394,7 +408,10 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* bar_n_empty = bar_n_full + C::kNotes;     // [kNotes]
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-  volatile int2* notes = reinterpret_cast<volatile int2*>(smem + C::kOffMisc + 16);   // {note, unit}
+  uint64_t* bar_w_full = bar_n_empty + C::kNotes;     // [kVNotes]
+  uint64_t* bar_w_empty = bar_w_full + C::kVNotes;    // [kVNotes]
+  volatile int* notes = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);     // [kNotes] {x, unit, n, masked}
+  volatile int* v_notes = notes + 4 * C::kNotes;                                      // [kVNotes] {x, unit, running tile, -}
   int* ids = reinterpret_cast<int*>(smem + C::kOffIds);
   uint32_t* bad = reinterpret_cast<uint32_t*>(smem + C::kOffBad);
   uint8_t* sQ = smem;
@@ -425,6 +442,10 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(bar_n_full + s, 1);
       mbar_init(bar_n_empty + s, C::kNoteReaders);
     }
+    for (int s = 0; s < C::kVNotes; ++s) {
+      mbar_init(bar_w_full + s, 1);
+      mbar_init(bar_w_empty + s, 2);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -437,11 +458,12 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
-  // The i-th note: {note, unit}.  Every reading warp frees its slot once (note_read).  Giving up reads as the end.
+  // The i-th note.  Every reading warp frees its slot once (note_read).  Giving up reads as the end.
+  struct Note { int x, unit, n, masked; };
   auto note_at = [&](int i) {
     const int slot = i % C::kNotes;
-    if (!mbar_wait(bar_n_full + slot, (i / C::kNotes) & 1, abort_flag, tmo, 0x2D)) return make_int2(kNoteEmpty, -1);
-    return make_int2(notes[slot].x, notes[slot].y);
+    if (!mbar_wait(bar_n_full + slot, (i / C::kNotes) & 1, abort_flag, tmo, 0x2D)) return Note{kNoteEmpty, -1, 0, 0};
+    return Note{notes[4 * slot], notes[4 * slot + 1], notes[4 * slot + 2], notes[4 * slot + 3]};
   };
   auto note_read = [&](int i) { mbar_arrive(bar_n_empty + i % C::kNotes); };
 
@@ -453,15 +475,27 @@ __global__ void __launch_bounds__(384, 1)
         tma_prefetch_desc(&maps.q[0]);
         tma_prefetch_desc(&maps.k[0]);
         tma_prefetch_desc(&maps.v[0]);
-        int g = 0, nq = 0, nn = 0, k_issued = 0, v_issued = 0;      // running tile, Q and note counts
+        int g = 0, nq = 0, nn = 0, nv = 0, k_issued = 0, v_issued = 0;   // running tile, Q and note counts
         bool ok = true;
-        auto put = [&](int note, int u) {
+        auto put = [&](int x, int u, int n, bool masked) {
           const int slot = nn % C::kNotes;
           if (nn >= C::kNotes && !mbar_wait(bar_n_empty + slot, ((nn / C::kNotes) + 1) & 1, abort_flag, tmo, 0x2E)) return false;
-          notes[slot].x = note;
-          notes[slot].y = u;
+          notes[4 * slot] = x;
+          notes[4 * slot + 1] = u;
+          notes[4 * slot + 2] = n;
+          notes[4 * slot + 3] = masked;
           mbar_arrive(bar_n_full + slot);
           ++nn;
+          return true;
+        };
+        auto put_v = [&](int x, int u) {
+          const int slot = nv % C::kVNotes;
+          if (nv >= C::kVNotes && !mbar_wait(bar_w_empty + slot, ((nv / C::kVNotes) + 1) & 1, abort_flag, tmo, 0x2F)) return false;
+          v_notes[4 * slot] = x;
+          v_notes[4 * slot + 1] = u;
+          v_notes[4 * slot + 2] = g;
+          mbar_arrive(bar_w_full + slot);
+          ++nv;
           return true;
         };
         int u = blockIdx.x;
@@ -471,10 +505,11 @@ __global__ void __launch_bounds__(384, 1)
                                          : u + static_cast<int>(gridDim.x);
           MaskedWalk<SPLIT> walk(p, w);
           const int kv = w.b * p.H_kv + (w.run % (p.H / p.run_heads)) * p.run_heads / (p.H / p.H_kv);
-          int note = 0, ahead = 0;
-          bool more = walk.next(ahead);
+          int ahead = 0, ahead_run = 0;
+          bool ahead_masked = false;
+          bool more = walk.next(ahead, ahead_run, ahead_masked);
           if (!more) {
-            ok = put(kNoteEmpty, u);
+            ok = put(kNoteEmpty, u, 0, false);
           } else {
             if (nq > 0 && !(ok = mbar_wait(bar_q_empty, (nq - 1) & 1, abort_flag, tmo, 0x20))) break;
             const int nt = SPLIT || p.rows - w.r0 <= 128 ? 1 : 2;
@@ -486,27 +521,33 @@ __global__ void __launch_bounds__(384, 1)
             ++nq;
           }
           while (ok && more) {
-            note = ahead;
-            more = walk.next(ahead);
-            if (!(ok = put(note | (more ? 0 : kNoteLast), u))) break;
-            const int j = note & kNoteTile;
-            const int st = g % NS;
-            if (g >= NS && !(ok = mbar_wait(bar_k_empty + st, ((g / NS) + 1) & 1, abort_flag, tmo, 0x21))) break;
-            mbar_arrive_expect_tx(bar_k_full + st, C::kTileBytes);
-            for (int b = 0; b < C::kNBlk; ++b)
-              tma_load_4d(sK + st * C::kTileBytes + b * C::kBlkBytes, &maps.k[0], bar_k_full + st, b * 64,
-                          j * kMaskedTile, kv, 0);
-            k_issued = g + 1;
-            if (g >= NS && !(ok = mbar_wait(bar_v_empty + st, ((g / NS) + 1) & 1, abort_flag, tmo, 0x22))) break;
-            mbar_arrive_expect_tx(bar_v_full + st, C::kTileBytes);
-            for (int b = 0; b < C::kNBlk; ++b)
-              tma_load_4d(sV + st * C::kTileBytes + b * C::kBlkBytes, &maps.v[0], bar_v_full + st, b * 64,
-                          j * kMaskedTile, kv, 0);
-            v_issued = ++g;
+            const int note = ahead;
+            int run = ahead_run;
+            const bool masked = ahead_masked;
+            more = walk.next(ahead, ahead_run, ahead_masked);
+            if (!(ok = put(note | (more ? 0 : kNoteLast), u, run, masked))) break;
+            if (masked && !(ok = put_v(note, u))) break;
+            const int step = run < 0 ? -1 : 1;
+            for (int j = note & kNoteTile; run != 0; j += step, run -= step) {
+              const int st = g % NS;
+              if (g >= NS && !(ok = mbar_wait(bar_k_empty + st, ((g / NS) + 1) & 1, abort_flag, tmo, 0x21))) break;
+              mbar_arrive_expect_tx(bar_k_full + st, C::kTileBytes);
+              for (int b = 0; b < C::kNBlk; ++b)
+                tma_load_4d(sK + st * C::kTileBytes + b * C::kBlkBytes, &maps.k[0], bar_k_full + st, b * 64,
+                            j * kMaskedTile, kv, 0);
+              k_issued = g + 1;
+              if (g >= NS && !(ok = mbar_wait(bar_v_empty + st, ((g / NS) + 1) & 1, abort_flag, tmo, 0x22))) break;
+              mbar_arrive_expect_tx(bar_v_full + st, C::kTileBytes);
+              for (int b = 0; b < C::kNBlk; ++b)
+                tma_load_4d(sV + st * C::kTileBytes + b * C::kBlkBytes, &maps.v[0], bar_v_full + st, b * 64,
+                            j * kMaskedTile, kv, 0);
+              v_issued = ++g;
+            }
           }
           u = u_next;
         }
-        if (ok) put(kNoteEmpty, -1);
+        if (ok) ok = put(kNoteEmpty, -1, 0, false);
+        if (ok) put_v(kNoteEmpty, -1);
         // the last load of every stage must land before the CTA may exit
         if (nq > 0) mbar_wait_drain(bar_q_full, (nq - 1) & 1, tmo);
         for (int r = 0; r < NS; ++r) {
@@ -546,8 +587,15 @@ __global__ void __launch_bounds__(384, 1)
         bool ok = true;
         int g = 0, nq = 0;                       // running tile and Q counts
         int np[2] = {0, 0};                      // P tiles taken from each stream
-        auto wait_v = [&](int gt) {
-          return mbar_wait(bar_v_clean + gt % NS, (gt / NS) & 1, abort_flag, tmo, 0x24);
+        // V of running tile gt: as it landed, or, of a masked tile, as the V warps left it.  They see masked tiles
+        // only; for the others this thread turns bar_v_clean in their place, so that its phases stay in step.
+        auto wait_v = [&](int gt, bool masked) {
+          const int vs = gt % NS, ph = (gt / NS) & 1;
+          if (masked) return mbar_wait(bar_v_clean + vs, ph, abort_flag, tmo, 0x24);
+          if (!mbar_wait(bar_v_full + vs, ph, abort_flag, tmo, 0x24)) return false;
+          mbar_arrive(bar_v_clean + vs);
+          mbar_arrive(bar_v_clean + vs);
+          return true;
         };
         auto wait_p = [&](int t) {
           const bool r = mbar_wait(bar_p_full + t, np[t] & 1, abort_flag, tmo, 0x25);
@@ -555,8 +603,8 @@ __global__ void __launch_bounds__(384, 1)
           return r;
         };
         for (int i = 0; ok;) {
-          int2 e = note_at(i);
-          if (e.y < 0) break;
+          Note e = note_at(i);
+          if (e.unit < 0) break;
           if (e.x & kNoteEmpty) {
             note_read(i++);
             continue;
@@ -565,56 +613,61 @@ __global__ void __launch_bounds__(384, 1)
           ++nq;
           int n = 0;                             // tiles of this unit so far
           int prev = 0, begun = 0;               // streams that own the previous tile, that have begun their O
+          bool prev_masked = false, prev2_masked = false;
           while (true) {
             note_read(i++);
-            const int st = g % NS;
-            if (!(ok = mbar_wait(bar_k_full + st, (g / NS) & 1, abort_flag, tmo, 0x23))) break;
-            tc_fence_after();
-            if constexpr (SPLIT) {
-              // stream t takes every other tile; its previous one is two back
-              const int t = n & 1;
-              if (n >= 2) {
-                if (!(ok = wait_v(g - 2) && wait_p(t))) break;
-                tc_fence_after();
-                issue_pv(t, (g - 2) % NS, n >= 4);
-                tc_commit(bar_v_empty + (g - 2) % NS);
-              }
-              issue_s(t, st);
-              tc_commit(bar_s_full + t);
-            } else {
-              const int vs = (g - 1 + NS) % NS;
-              if (prev && !(ok = wait_v(g - 1))) break;
-              const int own = (note_class(e.x, 0) != kNoteNone ? 1 : 0) | (note_class(e.x, 1) != kNoteNone ? 2 : 0);
-#pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                if (prev & (1 << t)) {
-                  if (!(ok = wait_p(t))) break;
+            const int own = (note_class(e.x, 0) != kNoteNone ? 1 : 0) | (note_class(e.x, 1) != kNoteNone ? 2 : 0);
+            for (int left = e.n < 0 ? -e.n : e.n; left > 0; --left) {
+              const int st = g % NS;
+              if (!(ok = mbar_wait(bar_k_full + st, (g / NS) & 1, abort_flag, tmo, 0x23))) break;
+              tc_fence_after();
+              if constexpr (SPLIT) {
+                // stream t takes every other tile; its previous one is two back
+                const int t = n & 1;
+                if (n >= 2) {
+                  if (!(ok = wait_v(g - 2, prev2_masked) && wait_p(t))) break;
                   tc_fence_after();
-                  issue_pv(t, vs, begun & (1 << t));
-                  begun |= 1 << t;
+                  issue_pv(t, (g - 2) % NS, n >= 4);
+                  tc_commit(bar_v_empty + (g - 2) % NS);
                 }
-                if (t == 1 && prev) tc_commit(bar_v_empty + vs);
-                if (own & (1 << t)) {
-                  issue_s(t, st);
-                  tc_commit(bar_s_full + t);
+                issue_s(t, st);
+                tc_commit(bar_s_full + t);
+                prev2_masked = prev_masked;
+              } else {
+                const int vs = (g - 1 + NS) % NS;
+                if (prev && !(ok = wait_v(g - 1, prev_masked))) break;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                  if (prev & (1 << t)) {
+                    if (!(ok = wait_p(t))) break;
+                    tc_fence_after();
+                    issue_pv(t, vs, begun & (1 << t));
+                    begun |= 1 << t;
+                  }
+                  if (t == 1 && prev) tc_commit(bar_v_empty + vs);
+                  if (own & (1 << t)) {
+                    issue_s(t, st);
+                    tc_commit(bar_s_full + t);
+                  }
                 }
+                if (!ok) break;
+                prev = own;
               }
-              if (!ok) break;
-              prev = own;
+              prev_masked = e.masked;
+              tc_commit(bar_k_empty + st);
+              ++g;
+              ++n;
             }
-            tc_commit(bar_k_empty + st);
-            ++g;
-            ++n;
-            if (e.x & kNoteLast) break;
+            if (!ok || (e.x & kNoteLast)) break;
             e = note_at(i);
-            if (!(ok = e.y >= 0)) break;
+            if (!(ok = e.unit >= 0)) break;
           }
           if (!ok) break;
           tc_commit(bar_q_empty);                // every S MMA of this unit is issued
           if constexpr (SPLIT) {
             for (int k = n >= 2 ? n - 2 : 0; ok && k < n; ++k) {
               const int t = k & 1, gt = g - n + k;
-              if (!(ok = wait_v(gt) && wait_p(t))) break;
+              if (!(ok = wait_v(gt, k == n - 1 ? prev_masked : prev2_masked) && wait_p(t))) break;
               tc_fence_after();
               issue_pv(t, gt % NS, k >= 2);
               tc_commit(bar_o_final + t);
@@ -622,7 +675,7 @@ __global__ void __launch_bounds__(384, 1)
             }
           } else {
             const int vs = (g - 1) % NS;
-            ok = wait_v(g - 1);
+            ok = wait_v(g - 1, prev_masked);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (ok && (prev & (1 << t))) {
@@ -646,27 +699,27 @@ __global__ void __launch_bounds__(384, 1)
       // warp 10 keys 0-63, warp 11 keys 64-127: document ids for the softmax, non-finite values zeroed
       const int half = warp - C::kVWarp;
       bool ok = true;
-      int g = 0;
       for (int i = 0; ok; ++i) {
-        const int2 e = note_at(i);
+        const int slot = i % C::kVNotes;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_w_full + slot, (i / C::kVNotes) & 1, abort_flag, tmo, 0x30));
+        if (!ok) break;
+        const int x = v_notes[4 * slot], unit = v_notes[4 * slot + 1], g = v_notes[4 * slot + 2];
         __syncwarp();
-        if (__any_sync(0xffffffffu, e.y < 0)) break;
-        if (lane == 0) note_read(i);
-        if (e.x & kNoteEmpty) continue;
-        const bool part = e.x & kNoteMasked;
-        const bool docs = p.words != nullptr && ((note_class(e.x, 0) | note_class(e.x, 1)) & kNoteDocs);
+        if (__any_sync(0xffffffffu, unit < 0)) break;
+        if (lane == 0) mbar_arrive(bar_w_empty + slot);
+        const bool docs = p.words != nullptr && ((note_class(x, 0) | note_class(x, 1)) & kNoteDocs);
         {
           const int st = g % NS;
           int id0 = -1, id1 = -1;
           if (docs) {
-            const int k = (e.x & kNoteTile) * kMaskedTile + half * 64 + lane;
-            const int* kd = p.kv_doc + static_cast<size_t>(masked_unit<SPLIT>(p, e.y).b) * p.S_kv;
+            const int k = (x & kNoteTile) * kMaskedTile + half * 64 + lane;
+            const int* kd = p.kv_doc + static_cast<size_t>(masked_unit<SPLIT>(p, unit).b) * p.S_kv;
             if (k < p.S_kv) id0 = max(__ldg(kd + k), -1);
             if (k + 32 < p.S_kv) id1 = max(__ldg(kd + k + 32), -1);
           }
           ok = __all_sync(0xffffffffu, mbar_wait(bar_v_full + st, (g / NS) & 1, abort_flag, tmo, 0x27));
           if (!ok) break;
-          if (part) {
+          {
             if (docs) {
               ids[st * 128 + half * 64 + lane] = id0;
               ids[st * 128 + half * 64 + 32 + lane] = id1;
@@ -679,18 +732,18 @@ __global__ void __launch_bounds__(384, 1)
             for (int b = 0; b < C::kNBlk; ++b) {
               uint4* base = reinterpret_cast<uint4*>(sV + st * C::kTileBytes + b * C::kBlkBytes + half * 8192);
 #pragma unroll 4
-              for (int i = 0; i < 16; ++i) {
-                const uint4 x = base[i * 32 + lane];
-                const uint32_t e = ((x.x & 0x7F807F80u) + 0x00800080u) | ((x.y & 0x7F807F80u) + 0x00800080u) |
-                                   ((x.z & 0x7F807F80u) + 0x00800080u) | ((x.w & 0x7F807F80u) + 0x00800080u);
+              for (int r4 = 0; r4 < 16; ++r4) {
+                const uint4 q = base[r4 * 32 + lane];
+                const uint32_t e = ((q.x & 0x7F807F80u) + 0x00800080u) | ((q.y & 0x7F807F80u) + 0x00800080u) |
+                                   ((q.z & 0x7F807F80u) + 0x00800080u) | ((q.w & 0x7F807F80u) + 0x00800080u);
                 if (e & 0x80008000u) {
                   auto clean = [](uint32_t v) {
                     if ((v & 0x7F80u) == 0x7F80u) v &= 0xFFFF0000u;
                     if ((v & 0x7F800000u) == 0x7F800000u) v &= 0x0000FFFFu;
                     return v;
                   };
-                  base[i * 32 + lane] = make_uint4(clean(x.x), clean(x.y), clean(x.z), clean(x.w));
-                  const int r = i * 4 + (lane >> 3);             // key within this half
+                  base[r4 * 32 + lane] = make_uint4(clean(q.x), clean(q.y), clean(q.z), clean(q.w));
+                  const int r = r4 * 4 + (lane >> 3);             // key within this half
                   atomicOr(&bad[st * 4 + half * 2 + (r >> 5)], 1u << (r & 31));
                 }
               }
@@ -699,7 +752,6 @@ __global__ void __launch_bounds__(384, 1)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_v_clean + st);
-          ++g;
         }
       }
     }
@@ -722,11 +774,10 @@ __global__ void __launch_bounds__(384, 1)
     int g = 0, ns = 0, no = 0;                   // running tiles of the CTA, S tiles and O's of this stream
 
     for (int i = 0; ok;) {
-      int2 e = note_at(i);
+      Note e = note_at(i);
       __syncwarp();
-      if (__any_sync(0xffffffffu, e.y < 0)) break;
-      const int u = e.y;
-      const MaskedUnit w = masked_unit<SPLIT>(p, u);
+      if (__any_sync(0xffffffffu, e.unit < 0)) break;
+      const MaskedUnit w = masked_unit<SPLIT>(p, e.unit);
       const int r = w.r0 + (SPLIT ? 0 : t * 128) + row;
       const bool valid_row = r < p.rows;
       const bool warp_rows = __any_sync(0xffffffffu, valid_row);
@@ -752,6 +803,7 @@ __global__ void __launch_bounds__(384, 1)
       auto take = [&] {
         const bool mine = SPLIT ? (n & 1) == t : note_class(e.x, t) != kNoteNone;
         ++n;
+        ++g;
         if (!mine) return false;
         ok = __all_sync(0xffffffffu, mbar_wait(bar_s_full + t, ns & 1, abort_flag, tmo, 0x28 + t));
         ++ns;
@@ -785,13 +837,12 @@ __global__ void __launch_bounds__(384, 1)
       };
       // The next note of this unit, false after its last.
       auto advance = [&] {
-        ++g;
         __syncwarp();
         if (lane == 0) note_read(i);
         ++i;
         if (e.x & kNoteLast) return false;
         e = note_at(i);
-        ok = __all_sync(0xffffffffu, e.y >= 0);
+        ok = __all_sync(0xffffffffu, e.unit >= 0);
         return ok;
       };
       // Distance bias of a tile to one side of the row: slope times the distance is linear in the column; a multiply-add
@@ -824,12 +875,12 @@ __global__ void __launch_bounds__(384, 1)
       while (more && !__any_sync(0xffffffffu, e.x & kNoteWhole)) {
         if (take()) {
           if (warp_rows) {
-            const int cls = note_class(e.x, t), j = e.x & kNoteTile, st = g % NS;
+            const int cls = note_class(e.x, t), j = e.x & kNoteTile, st = (g - 1) % NS;
             const bool docs = cls & kNoteDocs;
             const int valid = cls & kNoteRange ? lim - j * kMaskedTile : kMaskedTile;
             const int d = pos - j * kMaskedTile;
-            if (e.x & kNoteMasked) {
-              ok = __all_sync(0xffffffffu, mbar_wait(bar_v_clean + st, (g / NS) & 1, abort_flag, tmo, 0x2A));
+            if (e.masked) {
+              ok = __all_sync(0xffffffffu, mbar_wait(bar_v_clean + st, ((g - 1) / NS) & 1, abort_flag, tmo, 0x2A));
               if (!ok) break;
               for (int q = 0; q < 4; ++q)
                 for (uint32_t m = bad[st * 4 + q]; m != 0u; m &= m - 1u) {
@@ -885,7 +936,13 @@ __global__ void __launch_bounds__(384, 1)
       }
       // ---- whole tiles
       while (more && ok) {
-        if (take()) {
+        int j = e.x & kNoteTile;
+        const int step = e.n < 0 ? -1 : 1;
+        for (int left = e.n * step; left > 0; --left, j += step) {
+          if (!take()) {
+            if (!ok) break;
+            continue;
+          }
           if (warp_rows) {
             uint32_t s[128], pw[64];
             float sum = 0.0f, alpha = 1.0f, off = 0.0f;
@@ -893,7 +950,7 @@ __global__ void __launch_bounds__(384, 1)
             auto scores = [&] {
               tmem_ld128_sync(tS, s);
               if (capped) cap_scores(s, cap_c);
-              if (MOD == 2) off = tilt_scores(s, pos - (e.x & kNoteTile) * kMaskedTile);
+              if (MOD == 2) off = tilt_scores(s, pos - j * kMaskedTile);
             };
             scores();
             bool slow = !started;
