@@ -235,6 +235,7 @@ template <bool SPLIT>
 __global__ void __launch_bounds__(256) masked_tiles_kernel(const MaskedParams p) {
   __shared__ int red[3][8];
   __shared__ uint4 part[8];
+  grid_dep_launch();
   const int blk = blockIdx.x % p.n_blk, b = blockIdx.x / p.n_blk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_words = (p.S_kv + 32 * kMaskedTile - 1) / (32 * kMaskedTile);
@@ -422,6 +423,7 @@ __global__ void __launch_bounds__(384, 1)
   const int lane = threadIdx.x & 31;
   const uint64_t tmo = p.timeout_ns;
 
+  if (SPLIT) grid_dep_launch();                  // the join may take its place as soon as CTAs leave
   if (threadIdx.x == C::kTmaWarp * 32) {
     mbar_init(bar_q_full, 1);
     mbar_init(bar_q_empty, 1);
@@ -475,6 +477,7 @@ __global__ void __launch_bounds__(384, 1)
         tma_prefetch_desc(&maps.q[0]);
         tma_prefetch_desc(&maps.k[0]);
         tma_prefetch_desc(&maps.v[0]);
+        grid_dep_wait();                         // (the tile bits and the unit counter of this call)
         int g = 0, nq = 0, nn = 0, nv = 0, k_issued = 0, v_issued = 0;   // running tile, Q and note counts
         bool ok = true;
         auto put = [&](int x, int u, int n, bool masked) {
@@ -1038,6 +1041,7 @@ __global__ void __launch_bounds__(128) masked_join_kernel(const MaskedParams p) 
   const long long n_rows = static_cast<long long>(p.B) * p.H * p.S_q;
   const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   if (row >= n_rows) return;
+  grid_dep_wait();
   const int n = 2 * p.n_split;
   float M = -INFINITY;
   bool nan = false;

@@ -386,10 +386,12 @@ int launch_rope(const RopeParams& prm, bool e4m3, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? DIT_OK : DIT_ERR_CUDA;
 }
 
-// How the masked attention covers a call (host arithmetic on sizes only: the workspace is sized by it).
-// Cost model in steps of the long form (256 rows against 128 keys, about a microsecond): the long form
-// takes every KV tile of its unit in one CTA; the split form shares them between CTAs, two tiles of
-// 128 rows side by side in each, and pays for its units' start and for the join.  kMaskedSlots is the
+// How the masked attention covers a call (host arithmetic on sizes only: the workspace is sized by it): the form
+// with the smaller estimate, in microseconds as measured on a B200 without masks.  Long form: 2.0 a KV tile for
+// 256 rows (24 x 4608 x 128: 219 us in 3 x 36 tiles a CTA), 1.4 where a unit has one Q tile.  Split form: 0.95
+// a KV tile in a CTA, or what HBM gives all CTAs together (9.6 ns a CTA and 64 KB), 5 for a unit and 8 for the join:
+// one query of 4 x 40(8) heads x 32760 keys takes 91 us in 128 shares, 101 in 288, 138 in 64; 32 queries of 2 x
+// 8 heads x 4096 keys, D = 64, 19 us in 128 shares, 40 in 16, and 53 in the long form.  kMaskedSlots is the
 // SM count of a B200, a constant so that the workspace does not depend on the current device.
 constexpr int kMaskedSlots = 148;
 
@@ -421,13 +423,15 @@ MaskedPlan masked_plan(int B, int H, int H_kv, int S_q, int S_kv, int D, bool do
   const int pack = own - S_q <= own / 8 ? 1 : G;
   const long long rows = static_cast<long long>(pack) * S_q, runs = static_cast<long long>(B) * H / pack;
   const long long blk = (rows + 255) / 256;
-  double best = waves(runs * blk) * (tiles * (rows > 128 ? 1.0 : 0.7) + 2.0);
+  double best = waves(runs * blk) * (tiles * (rows > 128 ? 2.0 : 1.4) + 4.0);
   // the split form always packs: its calls have few rows
   const long long rows_split = static_cast<long long>(G) * S_q, runs_split = static_cast<long long>(B) * H_kv;
   const long long blk_split = (rows_split + 127) / 128;
   for (long long ns = 1; ns <= 64 && 2 * ns <= tiles && runs_split * blk_split * ns <= 6 * kMaskedSlots; ++ns) {
     const long long per = (tiles + ns - 1) / ns;
-    const double cost = waves(runs_split * blk_split * ns) * (per * 0.6 + 2.0) + 6.0;
+    const long long units = runs_split * blk_split * ns;
+    const double tile = std::max(0.95, 9.6e-3 * D / 128.0 * std::min<long long>(units, kMaskedSlots));
+    const double cost = waves(units) * (per * tile + 5.0) + 8.0;
     if (cost < best) {
       best = cost;
       m.split = true;
@@ -481,18 +485,33 @@ int launch_masked(const void* q, const void* k, const void* v, const MaskedParam
   const int grid = std::min(prm.n_units, slots);
   MaskedParams pr = prm;
   if (pr.n_units <= grid) pr.next_unit = nullptr;
+  // the kernels of one call overlap at their ends (programmatic dependent launch)
+  cudaLaunchAttribute attr;
+  std::memset(&attr, 0, sizeof(attr));
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.stream = st;
+  cfg.attrs = &attr;
   if (pr.words != nullptr) {
     masked_tiles_kernel<SPLIT><<<pr.B * pr.n_blk, 256, 0, st>>>(pr);
     if (cudaGetLastError() != cudaSuccess) return DIT_ERR_CUDA;
+    cfg.numAttrs = 1;
   } else if (pr.next_unit != nullptr) {
     if (cudaMemsetAsync(pr.next_unit, 0, sizeof(unsigned int), st) != cudaSuccess) return DIT_ERR_CUDA;
   }
-  attn_masked_kernel<D, SPLIT, MOD><<<grid, C::kThreads, C::kSmemBytes, st>>>(maps, pr);
-  if (cudaGetLastError() != cudaSuccess) return DIT_ERR_CUDA;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  if (cudaLaunchKernelEx(&cfg, attn_masked_kernel<D, SPLIT, MOD>, maps, pr) != cudaSuccess) return DIT_ERR_CUDA;
   if (SPLIT) {
     const long long n = static_cast<long long>(prm.runs) * prm.rows;
-    masked_join_kernel<D><<<static_cast<unsigned>((n + 3) / 4), 128, 0, st>>>(prm);
-    if (cudaGetLastError() != cudaSuccess) return DIT_ERR_CUDA;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>((n + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    if (cudaLaunchKernelEx(&cfg, masked_join_kernel<D>, pr) != cudaSuccess) return DIT_ERR_CUDA;
   }
   return DIT_OK;
 }
@@ -1171,6 +1190,8 @@ int dit_attn_fwd_masked(const void* q, const void* k, const void* v, void* out, 
   prm.part_o = reinterpret_cast<float*>(ws + plan.words_bytes);
   prm.part_lse = reinterpret_cast<float*>(ws + plan.words_bytes + plan.part_o_bytes);
   prm.timeout_ns = g_timeout_ns.load();
+  if (plan.split && slopes == nullptr && softcap == 0.0f)
+    return D == 64 ? launch_masked<64, true, 0>(q, k, v, prm, st) : launch_masked<128, true, 0>(q, k, v, prm, st);
   if (plan.split)
     return D == 64 ? launch_masked<64, true, 2>(q, k, v, prm, st) : launch_masked<128, true, 2>(q, k, v, prm, st);
   if (slopes != nullptr)

@@ -360,6 +360,11 @@ __host__ __device__ constexpr uint32_t instr_desc(uint32_t ab_format, bool b_mn_
          | ((static_cast<uint32_t>(M) >> 4) << 24);  // M / 16
 }
 
+// Programmatic dependent launch: let the dependent grid start its CTAs; wait until the grids this one
+// depends on have completed (their memory is then visible; at once in an ordinary launch).
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Warpgroup-wide register re-split (all 128 threads of the warpgroup execute it).
 template <uint32_t N>
 __device__ __forceinline__ void regs_inc() {
