@@ -55,6 +55,8 @@ struct MaskedParams {
   int n_split;                      // split form: shares of the KV tiles
   int n_units;
   unsigned int* next_unit;          // units handed out beyond the first of every CTA (zero at launch); null: in steps
+  int* cost;                        // documents, more units than CTAs: [B, n_blk] tiles of each unit of rows
+  int* order;                       // and (b, unit of rows) by falling cost, as b * n_blk + unit; or null
   uint4* words;                     // [B, n_blk, ceil(S_kv / 4096)] {seen, whole} tile bits of Q tiles 0 and 1, or null
   float* part_o;                    // split form: [2 n_split, B * H * S_q, D]
   float* part_lse;                  // split form: [2 n_split, B * H * S_q]
@@ -73,34 +75,36 @@ struct MaskedUnit {
   int run, b, r0, blk, share;
 };
 
+// Units are handed out for all runs of a sequence at a time, the blocks of rows with the longest walks first: by
+// `order`, else (causal masks) the last rows first.
 template <bool SPLIT>
 __device__ __forceinline__ MaskedUnit masked_unit(const MaskedParams& p, int u) {
   MaskedUnit w;
-  if constexpr (SPLIT) {
-    w.share = u % p.n_split;
-    w.blk = (u / p.n_split) % p.n_blk;
-    w.run = u / p.n_split / p.n_blk;
-    w.r0 = w.blk * 128;
+  w.share = SPLIT ? u % p.n_split : 0;
+  if (SPLIT) u /= p.n_split;
+  const int per_b = p.H / p.run_heads, at = u / per_b;
+  if (p.order != nullptr) {
+    const int x = p.order[at];
+    w.b = x / p.n_blk;
+    w.blk = x - w.b * p.n_blk;
   } else {
-    // the last rows (of a causal mask: the longest walks) of every run first
-    w.share = 0;
-    w.blk = p.n_blk - 1 - u / p.runs;
-    w.run = u % p.runs;
-    w.r0 = w.blk * 256;
+    w.b = at % p.B;
+    w.blk = p.n_blk - 1 - at / p.B;
   }
-  w.b = w.run / (p.H / p.run_heads);
+  w.run = w.b * per_b + u % per_b;
+  w.r0 = w.blk * (SPLIT ? 128 : 256);
   return w;
 }
 
-// A note {x, unit, n, masked} on n KV tiles of a unit (|n| neighbours; n < 0: downwards), from the TMA thread to the
-// other roles.  masked: some row does not see some key.  x, low bits: the first tile; 3 bits for each Q tile (the
+// A note on n KV tiles of a unit (|n| neighbours; n < 0: downwards), from the TMA thread to the other roles; with the
+// unit's run, rows and share.  masked: some row does not see some key.  x, low bits: the first tile; 3 bits for each Q tile (the
 // split form: both the same); then what the note is.
 constexpr int kNoteTile = (1 << 23) - 1;           // S_kv <= 2^30
 constexpr int kNoteNone = 1, kNoteRange = 2, kNoteDocs = 4;   // sees nothing; some keys past a row's limit; ids to compare
 constexpr int kNoteShift = 23;                     // Q tile t's bits at kNoteShift + 3 t
 constexpr int kNoteWhole = 1 << 29;                // (a whole tile: no row masks a key, and it lies to one side of every row)
 constexpr int kNoteLast = 1 << 30;                 // the unit's last note
-constexpr int kNoteEmpty = static_cast<int>(1u << 31);   // no tile: a unit whose rows see nothing, or (unit < 0) the end
+constexpr int kNoteEmpty = static_cast<int>(1u << 31);   // no tile: a unit whose rows see nothing, or (run < 0) the end
 
 __device__ __forceinline__ int note_class(int note, int t) { return (note >> (kNoteShift + 3 * t)) & 7; }
 
@@ -119,9 +123,7 @@ struct MaskedWalk {
   int at;
   uint4 x;
 
-  __device__ __forceinline__ MaskedWalk(const MaskedParams& p, const MaskedUnit& w) {
-    const int start = p.q_start ? __ldg(p.q_start + w.b) : p.S_kv - p.S_q;
-    const int pre = p.prefix ? __ldg(p.prefix + w.b) : 0;
+  __device__ __forceinline__ MaskedWalk(const MaskedParams& p, const MaskedUnit& w, int start, int pre) {
     int lo[2], hi[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -269,6 +271,14 @@ __global__ void __launch_bounds__(256) masked_tiles_kernel(const MaskedParams p)
   const bool absent = !SPLIT && blk * 256 + 128 >= p.rows;   // no second Q tile: it does not keep tiles from being whole
   const int* kd = p.kv_doc + static_cast<size_t>(b) * p.S_kv;
   uint4* words = p.words + static_cast<size_t>(blockIdx.x) * n_words;
+  // tiles past the causal limit of the unit's last row do not count
+  int n_tiles = 0, cost = 0;
+  {
+    const int last = min((blk + 1) * (SPLIT ? 128 : 256), p.rows) - 1, first = blk * (SPLIT ? 128 : 256);
+    const int hi = first / p.S_q == last / p.S_q ? last % p.S_q : p.S_q - 1;
+    n_tiles = (masked_limit(p, (p.q_start ? p.q_start[b] : p.S_kv - p.S_q) + hi, p.prefix ? p.prefix[b] : 0) + kMaskedTile - 1) /
+              kMaskedTile;
+  }
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.next_unit != nullptr) *p.next_unit = 0u;
   // 32 tiles at a time, four to a warp: sixteen loads of a lane in flight
   for (int w = 0; w < n_words; ++w) {
@@ -306,9 +316,50 @@ __global__ void __launch_bounds__(256) masked_tiles_kernel(const MaskedParams p)
 #pragma unroll
       for (int i = 1; i < 8; ++i) { x.x |= part[i].x; x.y |= part[i].y; x.z |= part[i].z; x.w |= part[i].w; }
       words[w] = x;
+      const int left = n_tiles - w * 32;
+      if (left > 0) cost += __popc((x.x | x.z) & (left < 32 ? (1u << left) - 1u : 0xFFFFFFFFu));
     }
     __syncthreads();
   }
+  if (threadIdx.x == 0 && p.cost != nullptr) p.cost[blockIdx.x] = cost;
+}
+
+// Units by falling cost: a counting sort over 256 classes, one CTA.  (Units of one class come in any order: it
+// changes who computes what when, not what.)
+__global__ void __launch_bounds__(1024) masked_order_kernel(const MaskedParams p) {
+  __shared__ int most, at[256];
+  grid_dep_launch();
+  const int n = p.B * p.n_blk;
+  if (threadIdx.x == 0) most = 0;
+  if (threadIdx.x < 256) at[threadIdx.x] = 0;
+  __syncthreads();
+  grid_dep_wait();
+  int m = 0;
+  for (int i = threadIdx.x; i < n; i += 1024) m = max(m, p.cost[i]);
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) atomicMax(&most, m);
+  __syncthreads();
+  const int shift = max(0, 32 - __clz(most) - 8);
+  for (int i = threadIdx.x; i < n; i += 1024) atomicAdd(&at[p.cost[i] >> shift], 1);
+  __syncthreads();
+  if (threadIdx.x < 32) {                         // first place of each class, the largest class first
+    int c[8], sum = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      c[k] = sum;
+      sum += at[255 - (threadIdx.x * 8 + k)];
+    }
+    int before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, o);
+      if (static_cast<int>(threadIdx.x) >= o) before += y;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) at[255 - (threadIdx.x * 8 + k)] = before - sum + c[k];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += 1024) p.order[atomicAdd(&at[p.cost[i] >> shift], 1)] = i;
 }
 
 template <int D, bool SPLIT>
@@ -337,7 +388,7 @@ struct MaskedCfg {
   static constexpr int kVNotes = 2;                                 // notes on masked tiles for the V warps
   static constexpr int kNumBars = 2 + 5 * kStages + 6 + 1 + 2 * kNotes + 2 * kVNotes;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
-  static constexpr int kSmemBytes = kOffMisc + 16 + 16 * (kNotes + kVNotes) + 1024;
+  static constexpr int kSmemBytes = kOffMisc + 16 + 32 * kNotes + 16 * kVNotes + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
@@ -411,8 +462,9 @@ __global__ void __launch_bounds__(384, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   uint64_t* bar_w_full = bar_n_empty + C::kNotes;     // [kVNotes]
   uint64_t* bar_w_empty = bar_w_full + C::kVNotes;    // [kVNotes]
-  volatile int* notes = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);     // [kNotes] {x, unit, n, masked}
-  volatile int* v_notes = notes + 4 * C::kNotes;                                      // [kVNotes] {x, unit, running tile, -}
+  // [kNotes] {x, run, rows, share, n, masked, start, prefix}, [kVNotes] {x, b, running tile, -}
+  volatile int* notes = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 16);
+  volatile int* v_notes = notes + 8 * C::kNotes;
   int* ids = reinterpret_cast<int*>(smem + C::kOffIds);
   uint32_t* bad = reinterpret_cast<uint32_t*>(smem + C::kOffBad);
   uint8_t* sQ = smem;
@@ -461,11 +513,11 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t tmem_base = *tmem_holder;
 
   // The i-th note.  Every reading warp frees its slot once (note_read).  Giving up reads as the end.
-  struct Note { int x, unit, n, masked; };
+  struct Note { int x, run, n, masked; };
   auto note_at = [&](int i) {
-    const int slot = i % C::kNotes;
-    if (!mbar_wait(bar_n_full + slot, (i / C::kNotes) & 1, abort_flag, tmo, 0x2D)) return Note{kNoteEmpty, -1, 0, 0};
-    return Note{notes[4 * slot], notes[4 * slot + 1], notes[4 * slot + 2], notes[4 * slot + 3]};
+    volatile int* e = notes + 8 * (i % C::kNotes);
+    if (!mbar_wait(bar_n_full + i % C::kNotes, (i / C::kNotes) & 1, abort_flag, tmo, 0x2D)) return Note{kNoteEmpty, -1, 0, 0};
+    return Note{e[0], e[1], e[4], e[5]};
   };
   auto note_read = [&](int i) { mbar_arrive(bar_n_empty + i % C::kNotes); };
 
@@ -480,22 +532,29 @@ __global__ void __launch_bounds__(384, 1)
         grid_dep_wait();                         // (the tile bits and the unit counter of this call)
         int g = 0, nq = 0, nn = 0, nv = 0, k_issued = 0, v_issued = 0;   // running tile, Q and note counts
         bool ok = true;
-        auto put = [&](int x, int u, int n, bool masked) {
+        MaskedUnit w;
+        int start = 0, pre = 0;
+        auto put = [&](int x, int run, int n, bool masked) {
           const int slot = nn % C::kNotes;
           if (nn >= C::kNotes && !mbar_wait(bar_n_empty + slot, ((nn / C::kNotes) + 1) & 1, abort_flag, tmo, 0x2E)) return false;
-          notes[4 * slot] = x;
-          notes[4 * slot + 1] = u;
-          notes[4 * slot + 2] = n;
-          notes[4 * slot + 3] = masked;
+          volatile int* e = notes + 8 * slot;
+          e[0] = x;
+          e[1] = run;
+          e[2] = w.r0;
+          e[3] = w.share;
+          e[4] = n;
+          e[5] = masked;
+          e[6] = start;
+          e[7] = pre;
           mbar_arrive(bar_n_full + slot);
           ++nn;
           return true;
         };
-        auto put_v = [&](int x, int u) {
+        auto put_v = [&](int x, int b) {
           const int slot = nv % C::kVNotes;
           if (nv >= C::kVNotes && !mbar_wait(bar_w_empty + slot, ((nv / C::kVNotes) + 1) & 1, abort_flag, tmo, 0x2F)) return false;
           v_notes[4 * slot] = x;
-          v_notes[4 * slot + 1] = u;
+          v_notes[4 * slot + 1] = b;
           v_notes[4 * slot + 2] = g;
           mbar_arrive(bar_w_full + slot);
           ++nv;
@@ -503,16 +562,18 @@ __global__ void __launch_bounds__(384, 1)
         };
         int u = blockIdx.x;
         while (ok && u < p.n_units) {
-          const MaskedUnit w = masked_unit<SPLIT>(p, u);
+          w = masked_unit<SPLIT>(p, u);
+          start = p.q_start ? __ldg(p.q_start + w.b) : p.S_kv - p.S_q;
+          pre = p.prefix ? __ldg(p.prefix + w.b) : 0;
           const int u_next = p.next_unit ? static_cast<int>(gridDim.x + atomicAdd(p.next_unit, 1u))
                                          : u + static_cast<int>(gridDim.x);
-          MaskedWalk<SPLIT> walk(p, w);
+          MaskedWalk<SPLIT> walk(p, w, start, pre);
           const int kv = w.b * p.H_kv + (w.run % (p.H / p.run_heads)) * p.run_heads / (p.H / p.H_kv);
           int ahead = 0, ahead_run = 0;
           bool ahead_masked = false;
           bool more = walk.next(ahead, ahead_run, ahead_masked);
           if (!more) {
-            ok = put(kNoteEmpty, u, 0, false);
+            ok = put(kNoteEmpty, w.run, 0, false);
           } else {
             if (nq > 0 && !(ok = mbar_wait(bar_q_empty, (nq - 1) & 1, abort_flag, tmo, 0x20))) break;
             const int nt = SPLIT || p.rows - w.r0 <= 128 ? 1 : 2;
@@ -528,8 +589,8 @@ __global__ void __launch_bounds__(384, 1)
             int run = ahead_run;
             const bool masked = ahead_masked;
             more = walk.next(ahead, ahead_run, ahead_masked);
-            if (!(ok = put(note | (more ? 0 : kNoteLast), u, run, masked))) break;
-            if (masked && !(ok = put_v(note, u))) break;
+            if (!(ok = put(note | (more ? 0 : kNoteLast), w.run, run, masked))) break;
+            if (masked && !(ok = put_v(note, w.b))) break;
             const int step = run < 0 ? -1 : 1;
             for (int j = note & kNoteTile; run != 0; j += step, run -= step) {
               const int st = g % NS;
@@ -607,7 +668,7 @@ __global__ void __launch_bounds__(384, 1)
         };
         for (int i = 0; ok;) {
           Note e = note_at(i);
-          if (e.unit < 0) break;
+          if (e.run < 0) break;
           if (e.x & kNoteEmpty) {
             note_read(i++);
             continue;
@@ -663,7 +724,7 @@ __global__ void __launch_bounds__(384, 1)
             }
             if (!ok || (e.x & kNoteLast)) break;
             e = note_at(i);
-            if (!(ok = e.unit >= 0)) break;
+            if (!(ok = e.run >= 0)) break;
           }
           if (!ok) break;
           tc_commit(bar_q_empty);                // every S MMA of this unit is issued
@@ -706,9 +767,9 @@ __global__ void __launch_bounds__(384, 1)
         const int slot = i % C::kVNotes;
         ok = __all_sync(0xffffffffu, mbar_wait(bar_w_full + slot, (i / C::kVNotes) & 1, abort_flag, tmo, 0x30));
         if (!ok) break;
-        const int x = v_notes[4 * slot], unit = v_notes[4 * slot + 1], g = v_notes[4 * slot + 2];
+        const int x = v_notes[4 * slot], b = v_notes[4 * slot + 1], g = v_notes[4 * slot + 2];
         __syncwarp();
-        if (__any_sync(0xffffffffu, unit < 0)) break;
+        if (__any_sync(0xffffffffu, b < 0)) break;
         if (lane == 0) mbar_arrive(bar_w_empty + slot);
         const bool docs = p.words != nullptr && ((note_class(x, 0) | note_class(x, 1)) & kNoteDocs);
         {
@@ -716,7 +777,7 @@ __global__ void __launch_bounds__(384, 1)
           int id0 = -1, id1 = -1;
           if (docs) {
             const int k = (x & kNoteTile) * kMaskedTile + half * 64 + lane;
-            const int* kd = p.kv_doc + static_cast<size_t>(masked_unit<SPLIT>(p, unit).b) * p.S_kv;
+            const int* kd = p.kv_doc + static_cast<size_t>(b) * p.S_kv;
             if (k < p.S_kv) id0 = max(__ldg(kd + k), -1);
             if (k + 32 < p.S_kv) id1 = max(__ldg(kd + k + 32), -1);
           }
@@ -779,23 +840,26 @@ __global__ void __launch_bounds__(384, 1)
     for (int i = 0; ok;) {
       Note e = note_at(i);
       __syncwarp();
-      if (__any_sync(0xffffffffu, e.unit < 0)) break;
-      const MaskedUnit w = masked_unit<SPLIT>(p, e.unit);
-      const int r = w.r0 + (SPLIT ? 0 : t * 128) + row;
+      if (__any_sync(0xffffffffu, e.run < 0)) break;
+      volatile int* info = notes + 8 * (i % C::kNotes);
+      const int run = e.run, share = info[3];
+      const int r = info[2] + (SPLIT ? 0 : t * 128) + row;
       const bool valid_row = r < p.rows;
       const bool warp_rows = __any_sync(0xffffffffu, valid_row);
       int pos, lim = p.S_kv, doc = -2;            // (-2: no key's document, padding's is -1)
       float slope = 0.0f;
       {
-        const int token = r % p.S_q, head = w.run % (p.H / p.run_heads) * p.run_heads + r / p.S_q;
-        pos = (p.q_start ? __ldg(p.q_start + w.b) : p.S_kv - p.S_q) + token;
+        const int per_b = p.H / p.run_heads, b = run / per_b;
+        const int token = r % p.S_q;
+        pos = info[6] + token;
         if (valid_row) {
-          lim = masked_limit(p, pos, p.prefix ? __ldg(p.prefix + w.b) : 0);
+          lim = masked_limit(p, pos, info[7]);
           if (p.words != nullptr) {
-            doc = __ldg(p.q_doc + static_cast<size_t>(w.b) * p.S_q + token);
+            doc = __ldg(p.q_doc + static_cast<size_t>(b) * p.S_q + token);
             if (doc < 0) doc = -2;
           }
-          if (MOD == 2 && p.slopes != nullptr) slope = __ldg(p.slopes + head) / unit;
+          if (MOD == 2 && p.slopes != nullptr)
+            slope = __ldg(p.slopes + (run - b * per_b) * p.run_heads + r / p.S_q) / unit;
         }
       }
       float m_use = valid_row ? -INFINITY : 0.0f, l = 0.0f;      // (rows past the end ride along with zero scores)
@@ -845,7 +909,7 @@ __global__ void __launch_bounds__(384, 1)
         ++i;
         if (e.x & kNoteLast) return false;
         e = note_at(i);
-        ok = __all_sync(0xffffffffu, e.unit >= 0);
+        ok = __all_sync(0xffffffffu, e.run >= 0);
         return ok;
       };
       // Distance bias of a tile to one side of the row: slope times the distance is linear in the column; a multiply-add
@@ -985,10 +1049,10 @@ __global__ void __launch_bounds__(384, 1)
       const bool empty = own == 0 || l == 0.0f;                  // no key was visible
       const float inv = empty ? 0.0f : 1.0f / l;
       const float lse = empty ? -INFINITY : unit * m_use + logf(l);
-      const size_t row_idx = static_cast<size_t>(w.run) * p.rows + r;
+      const size_t row_idx = static_cast<size_t>(run) * p.rows + r;
       if constexpr (SPLIT) {
         const size_t n_rows = static_cast<size_t>(p.runs) * p.rows;
-        const size_t at = static_cast<size_t>(2 * w.share + t) * n_rows + row_idx;
+        const size_t at = static_cast<size_t>(2 * share + t) * n_rows + row_idx;
         if (valid_row) p.part_lse[at] = lse;
         if (own > 0)
 #pragma unroll 1

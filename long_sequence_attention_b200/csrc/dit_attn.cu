@@ -407,8 +407,8 @@ struct MaskedPlan {
   bool split;
   int run_heads, runs, rows, n_blk, n_split;
   long long units;
-  size_t next_bytes, words_bytes, part_o_bytes, part_lse_bytes;
-  size_t total() const { return next_bytes + words_bytes + part_o_bytes + part_lse_bytes; }
+  size_t next_bytes, order_bytes, words_bytes, part_o_bytes, part_lse_bytes;
+  size_t total() const { return next_bytes + order_bytes + words_bytes + part_o_bytes + part_lse_bytes; }
 };
 
 MaskedPlan masked_plan(int B, int H, int H_kv, int S_q, int S_kv, int D, bool docs) {
@@ -445,6 +445,7 @@ MaskedPlan masked_plan(int B, int H, int H_kv, int S_q, int S_kv, int D, bool do
   m.units = static_cast<long long>(m.runs) * m.n_blk * (m.split ? m.n_split : 1);
   auto pad = [](size_t n) { return (n + 255) / 256 * 256; };
   m.next_bytes = 256;
+  if (docs) m.order_bytes = pad(static_cast<size_t>(B) * m.n_blk * 8);
   if (docs) m.words_bytes = pad(static_cast<size_t>(B) * m.n_blk * ((tiles + 31) / 32) * 16);
   if (m.split) {
     const size_t n = static_cast<size_t>(2 * m.n_split) * m.runs * m.rows;
@@ -484,7 +485,10 @@ int launch_masked(const void* q, const void* k, const void* v, const MaskedParam
   const int slots = sms - reserve > 1 ? sms - reserve : 1;
   const int grid = std::min(prm.n_units, slots);
   MaskedParams pr = prm;
-  if (pr.n_units <= grid) pr.next_unit = nullptr;
+  if (pr.n_units <= grid) {                      // every unit has its CTA: no order, no counter
+    pr.next_unit = nullptr;
+    pr.cost = pr.order = nullptr;
+  }
   // the kernels of one call overlap at their ends (programmatic dependent launch)
   cudaLaunchAttribute attr;
   std::memset(&attr, 0, sizeof(attr));
@@ -498,6 +502,11 @@ int launch_masked(const void* q, const void* k, const void* v, const MaskedParam
     masked_tiles_kernel<SPLIT><<<pr.B * pr.n_blk, 256, 0, st>>>(pr);
     if (cudaGetLastError() != cudaSuccess) return DIT_ERR_CUDA;
     cfg.numAttrs = 1;
+    if (pr.order != nullptr) {
+      cfg.gridDim = dim3(1);
+      cfg.blockDim = dim3(1024);
+      if (cudaLaunchKernelEx(&cfg, masked_order_kernel, pr) != cudaSuccess) return DIT_ERR_CUDA;
+    }
   } else if (pr.next_unit != nullptr) {
     if (cudaMemsetAsync(pr.next_unit, 0, sizeof(unsigned int), st) != cudaSuccess) return DIT_ERR_CUDA;
   }
@@ -1186,6 +1195,11 @@ int dit_attn_fwd_masked(const void* q, const void* k, const void* v, void* out, 
   prm.run_heads = plan.run_heads; prm.runs = plan.runs;
   prm.next_unit = plan.next_bytes ? reinterpret_cast<unsigned int*>(ws) : nullptr;
   ws += plan.next_bytes;
+  if (q_doc != nullptr) {
+    prm.cost = reinterpret_cast<int*>(ws);
+    prm.order = prm.cost + static_cast<size_t>(B) * plan.n_blk;
+  }
+  ws += plan.order_bytes;
   prm.words = q_doc != nullptr ? reinterpret_cast<uint4*>(ws) : nullptr;
   prm.part_o = reinterpret_cast<float*>(ws + plan.words_bytes);
   prm.part_lse = reinterpret_cast<float*>(ws + plan.words_bytes + plan.part_o_bytes);
