@@ -23,9 +23,11 @@
 //     visible key; without a document of the rows, by bits that a small kernel writes before), and passes a
 //     note on each through shared memory to the other roles: per Q tile, whether it sees none of the
 //     tile (then that stream skips it), some of it, or all.  Neighbouring whole tiles share a note.
-//   * Tiles that some row sees in part come first.  They take one loop of the softmax, which rewrites S in
-//     TMEM (cap, bias, -inf) and takes the exact maximum; the whole tiles take another, the dense form's
-//     speculative one, whose registers are then free of the masks' state.
+//   * Tiles that some row sees in part come first.  They take one loop of the softmax, which masks S and
+//     takes the exact maximum; the whole tiles take another, the dense form's speculative one, whose
+//     registers are then free of the masks' state.  A row's mask is 128 bits: the keys below its limit, and
+//     those of its document, which a warp finds for all rows of one document at once (a ballot of 32 keys'
+//     ids a word).  Only 16-column pieces that some row of the warp does not see whole are touched.
 //   * The two idle warps of the dense form look through the V rows of tiles that are masked for some row: a
 //     non-finite value would reach every row of the tile (0 * inf), so it is zeroed in shared memory
 //     and its key flagged; the rows that may see that key become NaN, the others never notice.
@@ -368,8 +370,10 @@ struct MaskedCfg {
   static constexpr int kBlkBytes = 128 * 128;
   static constexpr int kNBlk = D / 64;
   static constexpr int kQTiles = SPLIT ? 1 : 2;
-  // D = 128: 2 Q + 2 K + 2 V tiles, or 1 + 3 + 3; D = 64: 2 + 5 + 5, or 1 + 6 + 6 (tiles of 16 KB)
-  static constexpr int kStages = D == 128 ? (SPLIT ? 3 : 2) : (SPLIT ? 6 : 5);
+  // Q tiles of the next unit while this one's are in use, where there is room: its first S then need not wait for them
+  static constexpr int kQBufs = D == 64 && !SPLIT ? 2 : 1;
+  // D = 128: 2 Q + 2 K + 2 V tiles, or 1 + 3 + 3; D = 64: 4 + 4 + 4, or 1 + 6 + 6 (tiles of 16 KB)
+  static constexpr int kStages = D == 128 ? (SPLIT ? 3 : 2) : (SPLIT ? 6 : 4);
   static constexpr int kThreads = 384;
   static constexpr int kRegsLaunch = 168, kRegsSoftmax = 216, kRegsCtl = 72;
   static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsCtl <= kThreads * kRegsLaunch, "register split");
@@ -378,7 +382,7 @@ struct MaskedCfg {
   // P, O and l are floating point, so a running maximum 2^40 below the true one costs no precision (dense form:
   // 2^8): loud scores then hardly ever leave the speculative path
   static constexpr float kRescaleLog2 = 40.0f, kSumBound = 1099511627776.0f;
-  static constexpr int kOffK = kQTiles * kTileBytes;
+  static constexpr int kOffK = kQBufs * kQTiles * kTileBytes;
   static constexpr int kOffV = kOffK + kStages * kTileBytes;
   static constexpr int kOffIds = kOffV + kStages * kTileBytes;      // documents of the tile's keys, per V stage
   static constexpr int kOffBad = kOffIds + kStages * 512;           // 128 bits of flagged keys, per V stage
@@ -386,7 +390,7 @@ struct MaskedCfg {
   static constexpr int kNotes = 4;                                   // notes not yet read by every role
   static constexpr int kNoteReaders = 1 + 8;                        // MMA and softmax warps
   static constexpr int kVNotes = 2;                                 // notes on masked tiles for the V warps
-  static constexpr int kNumBars = 2 + 5 * kStages + 6 + 1 + 2 * kNotes + 2 * kVNotes;
+  static constexpr int kNumBars = 2 * kQBufs + 5 * kStages + 6 + 1 + 2 * kNotes + 2 * kVNotes;
   static constexpr int kOffMisc = kOffBar + 8 * kNumBars;
   static constexpr int kSmemBytes = kOffMisc + 16 + 32 * kNotes + 16 * kVNotes + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
@@ -446,8 +450,9 @@ __global__ void __launch_bounds__(384, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint64_t* bar_q_full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  uint64_t* bar_q_empty = bar_q_full + 1;
-  uint64_t* bar_k_full = bar_q_full + 2;              // [NS]
+  constexpr int NQ = C::kQBufs;
+  uint64_t* bar_q_empty = bar_q_full + NQ;            // [NQ] (and bar_q_full)
+  uint64_t* bar_k_full = bar_q_empty + NQ;            // [NS]
   uint64_t* bar_k_empty = bar_k_full + NS;            // [NS]
   uint64_t* bar_v_full = bar_k_empty + NS;            // [NS] V has landed
   uint64_t* bar_v_clean = bar_v_full + NS;            // [NS] and holds finite values where it is masked
@@ -477,8 +482,10 @@ __global__ void __launch_bounds__(384, 1)
 
   if (SPLIT) grid_dep_launch();                  // the join may take its place as soon as CTAs leave
   if (threadIdx.x == C::kTmaWarp * 32) {
-    mbar_init(bar_q_full, 1);
-    mbar_init(bar_q_empty, 1);
+    for (int s = 0; s < NQ; ++s) {
+      mbar_init(bar_q_full + s, 1);
+      mbar_init(bar_q_empty + s, 1);
+    }
     for (int s = 0; s < NS; ++s) {
       mbar_init(bar_k_full + s, 1);
       mbar_init(bar_k_empty + s, 1);
@@ -574,16 +581,8 @@ __global__ void __launch_bounds__(384, 1)
           bool more = walk.next(ahead, ahead_run, ahead_masked);
           if (!more) {
             ok = put(kNoteEmpty, w.run, 0, false);
-          } else {
-            if (nq > 0 && !(ok = mbar_wait(bar_q_empty, (nq - 1) & 1, abort_flag, tmo, 0x20))) break;
-            const int nt = SPLIT || p.rows - w.r0 <= 128 ? 1 : 2;
-            mbar_arrive_expect_tx(bar_q_full, nt * C::kTileBytes);
-            for (int t = 0; t < nt; ++t)
-              for (int b = 0; b < C::kNBlk; ++b)
-                tma_load_4d(sQ + t * C::kTileBytes + b * C::kBlkBytes, &maps.q[0], bar_q_full, b * 64, w.r0 + t * 128,
-                            w.run, 0);
-            ++nq;
           }
+          bool q_here = false;
           while (ok && more) {
             const int note = ahead;
             int run = ahead_run;
@@ -600,6 +599,18 @@ __global__ void __launch_bounds__(384, 1)
                 tma_load_4d(sK + st * C::kTileBytes + b * C::kBlkBytes, &maps.k[0], bar_k_full + st, b * 64,
                             j * kMaskedTile, kv, 0);
               k_issued = g + 1;
+              if (!q_here) {                     // after the first K, which need not wait for the last unit's S
+                q_here = true;
+                const int qb = nq % NQ;
+                if (nq >= NQ && !(ok = mbar_wait(bar_q_empty + qb, ((nq / NQ) + 1) & 1, abort_flag, tmo, 0x20))) break;
+                const int nt = SPLIT || p.rows - w.r0 <= 128 ? 1 : 2;
+                mbar_arrive_expect_tx(bar_q_full + qb, nt * C::kTileBytes);
+                for (int t = 0; t < nt; ++t)
+                  for (int b = 0; b < C::kNBlk; ++b)
+                    tma_load_4d(sQ + (qb * C::kQTiles + t) * C::kTileBytes + b * C::kBlkBytes, &maps.q[0], bar_q_full + qb,
+                                b * 64, w.r0 + t * 128, w.run, 0);
+                ++nq;
+              }
               if (g >= NS && !(ok = mbar_wait(bar_v_empty + st, ((g / NS) + 1) & 1, abort_flag, tmo, 0x22))) break;
               mbar_arrive_expect_tx(bar_v_full + st, C::kTileBytes);
               for (int b = 0; b < C::kNBlk; ++b)
@@ -613,7 +624,8 @@ __global__ void __launch_bounds__(384, 1)
         if (ok) ok = put(kNoteEmpty, -1, 0, false);
         if (ok) put_v(kNoteEmpty, -1);
         // the last load of every stage must land before the CTA may exit
-        if (nq > 0) mbar_wait_drain(bar_q_full, (nq - 1) & 1, tmo);
+        for (int r = 0; r < NQ; ++r)
+          if (nq > r) mbar_wait_drain(bar_q_full + r, ((nq - 1 - r) / NQ) & 1, tmo);
         for (int r = 0; r < NS; ++r) {
           if (k_issued > r) mbar_wait_drain(bar_k_full + r, ((k_issued - 1 - r) / NS) & 1, tmo);
           if (v_issued > r) mbar_wait_drain(bar_v_full + r, ((v_issued - 1 - r) / NS) & 1, tmo);
@@ -630,8 +642,8 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t qk_hi = static_cast<uint32_t>(dq >> 32), v_hi = static_cast<uint32_t>(dv >> 32);
         const uint32_t q_lo = static_cast<uint32_t>(dq), k_lo = static_cast<uint32_t>(dk),
                        v_lo = static_cast<uint32_t>(dv);
-        auto issue_s = [&](int t, int st) {
-          const uint32_t a0 = q_lo + (((SPLIT ? 0 : t) * C::kTileBytes) >> 4);
+        auto issue_s = [&](int t, int st, int qb) {
+          const uint32_t a0 = q_lo + (((qb * C::kQTiles + (SPLIT ? 0 : t)) * C::kTileBytes) >> 4);
           const uint32_t b0 = k_lo + ((st * C::kTileBytes) >> 4);
           const uint32_t d = tmem_base + (t ? C::kColS1 : C::kColS0);
 #pragma unroll
@@ -673,7 +685,8 @@ __global__ void __launch_bounds__(384, 1)
             note_read(i++);
             continue;
           }
-          if (!(ok = mbar_wait(bar_q_full, nq & 1, abort_flag, tmo, 0x26))) break;
+          const int qb = nq % NQ;
+          if (!(ok = mbar_wait(bar_q_full + qb, (nq / NQ) & 1, abort_flag, tmo, 0x26))) break;
           ++nq;
           int n = 0;                             // tiles of this unit so far
           int prev = 0, begun = 0;               // streams that own the previous tile, that have begun their O
@@ -694,7 +707,7 @@ __global__ void __launch_bounds__(384, 1)
                   issue_pv(t, (g - 2) % NS, n >= 4);
                   tc_commit(bar_v_empty + (g - 2) % NS);
                 }
-                issue_s(t, st);
+                issue_s(t, st, qb);
                 tc_commit(bar_s_full + t);
                 prev2_masked = prev_masked;
               } else {
@@ -710,7 +723,7 @@ __global__ void __launch_bounds__(384, 1)
                   }
                   if (t == 1 && prev) tc_commit(bar_v_empty + vs);
                   if (own & (1 << t)) {
-                    issue_s(t, st);
+                    issue_s(t, st, qb);
                     tc_commit(bar_s_full + t);
                   }
                 }
@@ -727,7 +740,7 @@ __global__ void __launch_bounds__(384, 1)
             if (!(ok = e.run >= 0)) break;
           }
           if (!ok) break;
-          tc_commit(bar_q_empty);                // every S MMA of this unit is issued
+          tc_commit(bar_q_empty + qb);           // every S MMA of this unit is issued
           if constexpr (SPLIT) {
             for (int k = n >= 2 ? n - 2 : 0; ok && k < n; ++k) {
               const int t = k & 1, gt = g - n + k;
@@ -837,31 +850,39 @@ __global__ void __launch_bounds__(384, 1)
     bool ok = true;
     int g = 0, ns = 0, no = 0;                   // running tiles of the CTA, S tiles and O's of this stream
 
-    for (int i = 0; ok;) {
-      Note e = note_at(i);
-      __syncwarp();
-      if (__any_sync(0xffffffffu, e.run < 0)) break;
+    // A row of a unit: its place in its run, its position among the keys, the first key past those it may see, its
+    // document (-2: no key's; padding's is -1) and its slope in the scores' unit.
+    struct Row { int run, share, r, pos, lim, doc; float slope; };
+    auto row_of = [&](int i, int run) {
       volatile int* info = notes + 8 * (i % C::kNotes);
-      const int run = e.run, share = info[3];
-      const int r = info[2] + (SPLIT ? 0 : t * 128) + row;
+      Row q;
+      q.run = run;
+      q.share = info[3];
+      q.r = info[2] + (SPLIT ? 0 : t * 128) + row;
+      const int per_b = p.H / p.run_heads, b = run / per_b, token = q.r % p.S_q;
+      q.pos = info[6] + token;
+      q.lim = p.S_kv;
+      q.doc = -2;
+      q.slope = 0.0f;
+      if (run >= 0 && q.r < p.rows) {
+        if (p.words != nullptr) q.doc = max(__ldg(p.q_doc + static_cast<size_t>(b) * p.S_q + token), -2);
+        if (q.doc == -1) q.doc = -2;
+        q.lim = masked_limit(p, q.pos, info[7]);
+        if (MOD == 2 && p.slopes != nullptr)
+          q.slope = __ldg(p.slopes + (run - b * per_b) * p.run_heads + q.r / p.S_q) / unit;
+      }
+      return q;
+    };
+
+    int i = 0;
+    Note e = note_at(i);
+    __syncwarp();
+    Row q = row_of(i, e.run);
+    while (ok && !__any_sync(0xffffffffu, e.run < 0)) {
+      const int run = q.run, share = q.share, r = q.r, pos = q.pos, lim = q.lim, doc = q.doc;
+      const float slope = q.slope;
       const bool valid_row = r < p.rows;
       const bool warp_rows = __any_sync(0xffffffffu, valid_row);
-      int pos, lim = p.S_kv, doc = -2;            // (-2: no key's document, padding's is -1)
-      float slope = 0.0f;
-      {
-        const int per_b = p.H / p.run_heads, b = run / per_b;
-        const int token = r % p.S_q;
-        pos = info[6] + token;
-        if (valid_row) {
-          lim = masked_limit(p, pos, info[7]);
-          if (p.words != nullptr) {
-            doc = __ldg(p.q_doc + static_cast<size_t>(b) * p.S_q + token);
-            if (doc < 0) doc = -2;
-          }
-          if (MOD == 2 && p.slopes != nullptr)
-            slope = __ldg(p.slopes + (run - b * per_b) * p.run_heads + r / p.S_q) / unit;
-        }
-      }
       float m_use = valid_row ? -INFINITY : 0.0f, l = 0.0f;      // (rows past the end ride along with zero scores)
       bool poison = false, started = false;       // started: every row of the warp has seen a key
       int n = 0, own = 0;                         // tiles of the unit, and of this stream
@@ -943,56 +964,56 @@ __global__ void __launch_bounds__(384, 1)
         if (take()) {
           if (warp_rows) {
             const int cls = note_class(e.x, t), j = e.x & kNoteTile, st = (g - 1) % NS;
-            const bool docs = cls & kNoteDocs;
-            const int valid = cls & kNoteRange ? lim - j * kMaskedTile : kMaskedTile;
-            const int d = pos - j * kMaskedTile;
+            uint32_t see[4];                     // the row's keys of this tile
+            {
+              const int valid = cls & kNoteRange ? lim - j * kMaskedTile : kMaskedTile;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                see[k] = valid >= 32 * k + 32 ? 0xFFFFFFFFu : (valid <= 32 * k ? 0u : (1u << (valid - 32 * k)) - 1u);
+            }
             if (e.masked) {
               ok = __all_sync(0xffffffffu, mbar_wait(bar_v_clean + st, ((g - 1) / NS) & 1, abort_flag, tmo, 0x2A));
               if (!ok) break;
-              for (int q = 0; q < 4; ++q)
-                for (uint32_t m = bad[st * 4 + q]; m != 0u; m &= m - 1u) {
-                  const int c = q * 32 + __ffs(m) - 1;
-                  poison |= c < valid && (!docs || ids[st * 128 + c] == doc);
-                }
-            }
-            // Cap, bias and masks in passes of 32 columns, written back over S.
-            if (MOD == 2 || cls != 0) {
-#pragma unroll 1
-              for (int c0 = 0; c0 < kMaskedTile; c0 += 32) {
-                uint32_t x[32];
-                tmem_ld32_sync(tS + c0, x);
-                if (capped) cap_scores(x, cap_c);
-                if (MOD == 2) {
-                  const float df = static_cast<float>(d - c0);
+              if (cls & kNoteDocs) {
+                int id[4];
+                uint32_t same[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-                  for (int c = 0; c < 32; ++c)
-                    x[c] = __float_as_uint(fmaf(-slope, fabsf(df - static_cast<float>(c)), __uint_as_float(x[c])));
-                }
-                if (docs) {
-                  const int4* idp = reinterpret_cast<const int4*>(ids + st * 128 + c0);
+                for (int k = 0; k < 4; ++k) id[k] = ids[st * 128 + 32 * k + lane];
+                for (uint32_t todo = __ballot_sync(0xffffffffu, doc >= 0); todo != 0u;) {
+                  const int one = __shfl_sync(0xffffffffu, doc, __ffs(todo) - 1);
 #pragma unroll
-                  for (int c = 0; c < 8; ++c) {
-                    const int4 id = idp[c];
-                    if (id.x != doc) x[4 * c] = 0xFF800000u;
-                    if (id.y != doc) x[4 * c + 1] = 0xFF800000u;
-                    if (id.z != doc) x[4 * c + 2] = 0xFF800000u;
-                    if (id.w != doc) x[4 * c + 3] = 0xFF800000u;
+                  for (int k = 0; k < 4; ++k) {
+                    const uint32_t w = __ballot_sync(0xffffffffu, id[k] == one);
+                    if (doc == one) same[k] = w;
                   }
+                  todo &= ~__ballot_sync(0xffffffffu, doc == one);
                 }
-                if (__any_sync(0xffffffffu, valid < c0 + 32)) {
 #pragma unroll
-                  for (int c = 0; c < 32; ++c)
-                    if (c >= valid - c0) x[c] = 0xFF800000u;
-                }
-                tmem_st32(tS + c0, x);
+                for (int k = 0; k < 4; ++k) see[k] &= same[k];
               }
-              tmem_st_wait();
+#pragma unroll
+              for (int k = 0; k < 4; ++k) poison |= (see[k] & bad[st * 4 + k]) != 0u;
             }
             uint32_t s[128], pw[64];
             float sum = 0.0f, alpha = 1.0f;
             bool need = false;
             tmem_ld128_sync(tS, s);
-            if (MOD == 1 && cls == 0) cap_scores(s, cap_c);
+            if (capped) cap_scores(s, cap_c);
+            if (MOD == 2) {
+              const float df = static_cast<float>(pos - j * kMaskedTile);
+#pragma unroll
+              for (int c = 0; c < 128; ++c)
+                s[c] = __float_as_uint(fmaf(-slope, fabsf(df - static_cast<float>(c)), __uint_as_float(s[c])));
+            }
+#pragma unroll
+            for (int c0 = 0; c0 < 128; c0 += 16) {
+              const uint32_t w = (see[c0 >> 5] >> (c0 & 16)) & 0xFFFFu;
+              if (!__all_sync(0xffffffffu, w == 0xFFFFu)) {
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                  if (!((w >> c) & 1u)) s[c0 + c] = 0xFF800000u;
+              }
+            }
             exact(s, 0.0f, pw, sum, alpha, need);
             give(pw, sum, alpha, need);
           }
@@ -1036,6 +1057,11 @@ __global__ void __launch_bounds__(384, 1)
         more = advance();
       }
       if (!ok) break;
+
+      // the next unit's note and row, while the last P.V runs
+      e = note_at(i);
+      __syncwarp();
+      q = row_of(i, e.run);
 
       // ---------------------------------------------------------------- epilogue
       if (own > 0) {
