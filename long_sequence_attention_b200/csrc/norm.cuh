@@ -80,9 +80,10 @@ struct NormVec<float> {
   }
 };
 
-// N results to the output row at element e: bf16, fp32 (OUT 0, 1) or E4M3 codes of y / d (OUT 2).
+// N results to the output row at element e: bf16, fp32 (OUT 0, 1) or E4M3 codes of y / d (OUT 2), the quotient taken as
+// y times 1 / d correctly rounded: y carries roundings of that size anyhow.
 template <int OUT, int N>
-__device__ __forceinline__ void norm_store(void* out, long long e, const float (&y)[N], float d, float rcp) {
+__device__ __forceinline__ void norm_store(void* out, long long e, const float (&y)[N], float rcp) {
   if constexpr (OUT == 0) {
     uint32_t w[N / 2];
 #pragma unroll
@@ -98,8 +99,7 @@ __device__ __forceinline__ void norm_store(void* out, long long e, const float (
   } else {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      const uint32_t c = pack_e4m3x4(quot_e4m3(y[i], d, rcp), quot_e4m3(y[i + 1], d, rcp), quot_e4m3(y[i + 2], d, rcp),
-                                     quot_e4m3(y[i + 3], d, rcp));
+      const uint32_t c = pack_e4m3x4(y[i] * rcp, y[i + 1] * rcp, y[i + 2] * rcp, y[i + 3] * rcp);
       *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(out) + e + i) = c;
     }
   }
@@ -112,7 +112,7 @@ constexpr int kNormWarpVecs = 128;         // a warp of 4 pieces
 // Thread i of the row's group holds pieces i, i + width, ...: 128 columns are 16 (bf16) or 32 (fp32) neighbouring
 // lanes, so a scale of 128 columns is a few shuffles.
 template <typename T, int OUT, int NV, int LANES>
-__global__ void __launch_bounds__(LANES ? 256 : (NV <= 2 ? 1024 : 512)) rms_norm_vec_kernel(const NormParams p) {
+__global__ void __launch_bounds__(LANES ? 256 : (NV <= 2 ? 1024 : 512), LANES || NV != 4 ? 1 : 2) rms_norm_vec_kernel(const NormParams p) {
   using V = NormVec<T>;
   constexpr int N = V::kN;
   __shared__ float red[2][33];
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(LANES ? 256 : (NV <= 2 ? 1024 : 512)) rms_norm
   const long long base = row * p.C;
   const T* r = static_cast<const T*>(p.residual) + (p.residual ? base : 0);
   const T* w = static_cast<const T*>(p.weight);
-  uint4 xv[NV], rv[NV], wv[NV];
+  uint4 xv[NV], rv[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = at + i * width;
@@ -134,7 +134,6 @@ __global__ void __launch_bounds__(LANES ? 256 : (NV <= 2 ? 1024 : 512)) rms_norm
     if (on && v < nvec) {
       xv[i] = *reinterpret_cast<const uint4*>(x + v * N);
       if (p.residual) rv[i] = *reinterpret_cast<const uint4*>(r + v * N);
-      if (w) wv[i] = __ldg(reinterpret_cast<const uint4*>(w + v * N));
     }
   }
   float h[NV][N];
@@ -168,10 +167,16 @@ __global__ void __launch_bounds__(LANES ? 256 : (NV <= 2 ? 1024 : 512)) rms_norm
   const float inv = __frsqrt_rn(ss / static_cast<float>(p.C) + p.eps);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    float b[N];
-    if (w) V::unpack(wv[i], b);
+    const int v = at + i * width;
+    if (w) {
+      float b[N];
+      V::unpack(v < nvec ? __ldg(reinterpret_cast<const uint4*>(w + v * N)) : make_uint4(0u, 0u, 0u, 0u), b);
 #pragma unroll
-    for (int e = 0; e < N; ++e) h[i][e] = w ? h[i][e] * inv * b[e] : h[i][e] * inv;
+      for (int e = 0; e < N; ++e) h[i][e] = h[i][e] * inv * b[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) h[i][e] *= inv;
+    }
   }
   float d = 1.0f, rcp = 1.0f;
   if (OUT == 2 && p.group == p.C) {              // one scale a row
@@ -213,7 +218,7 @@ __global__ void __launch_bounds__(LANES ? 256 : (NV <= 2 ? 1024 : 512)) rms_norm
       rcp = __frcp_rn(d);
       if (on && v < nvec && v % kGroup == 0) p.descales[row * ((p.C + 127) / 128) + v / kGroup] = d;
     }
-    if (on && v < nvec) norm_store<OUT, N>(p.out, base + v * N, h[i], d, rcp);
+    if (on && v < nvec) norm_store<OUT, N>(p.out, base + v * N, h[i], rcp);
   }
 }
 
@@ -285,7 +290,7 @@ __global__ void __launch_bounds__(1024) rms_norm_cols_kernel(const NormParams p)
       if (c >= p.C) continue;
       if constexpr (OUT == 0) static_cast<__nv_bfloat16*>(p.out)[base + c] = __float2bfloat16(h[g][e]);
       else if constexpr (OUT == 1) static_cast<float*>(p.out)[base + c] = h[g][e];
-      else static_cast<uint8_t*>(p.out)[base + c] = static_cast<uint8_t>(pack_e4m3x2(quot_e4m3(h[g][e], d, rcp), 0.0f) & 0xFFu);
+      else static_cast<uint8_t*>(p.out)[base + c] = static_cast<uint8_t>(pack_e4m3x2(h[g][e] * rcp, 0.0f) & 0xFFu);
     }
   }
 }
