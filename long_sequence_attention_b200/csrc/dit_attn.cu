@@ -360,26 +360,38 @@ int launch_norm(const NormParams& prm, cudaStream_t st) {
   return launch_norm_vec<T, OUT, 8, 0>(prm, threads(8), st);
 }
 
-// Heads a CTA walks over: more reuse the angles, fewer fill the GPU.  About eight CTAs' worth of work for each
-// of the SMs (two for the E4M3 form, whose CTA fills half an SM) while at most 24 heads share the angles.
-int rope_heads_per(long long token_blocks, int heads, long long ctas) {
-  const long long groups = std::min<long long>(heads, (ctas + token_blocks - 1) / token_blocks);
-  const int per = static_cast<int>((heads + groups - 1) / groups);
-  return std::min(per, 24);
+// Heads a CTA walks over: more share the angles, fewer fill the GPU.  The number of CTAs per block of tokens that
+// takes the fewest rounds of `slots` resident CTAs, a CTA's start counted as 1.5 heads, at most 48 heads.
+int rope_heads_per(long long token_blocks, int heads, long long slots) {
+  int best = 1;
+  double best_cost = -1.0;
+  for (int per = 1; per <= std::min(heads, 48); ++per) {
+    const long long ctas = token_blocks * ((heads + per - 1) / per);
+    const double rounds = ctas <= 8 * slots ? static_cast<double>((ctas + slots - 1) / slots) : static_cast<double>(ctas) / slots;
+    const double cost = rounds * (per + 1.5);
+    if (best_cost < 0.0 || cost < best_cost) {
+      best_cost = cost;
+      best = per;
+    }
+  }
+  return best;
 }
 
 template <int D, bool INTER>
 int launch_rope(const RopeParams& prm, bool e4m3, cudaStream_t st) {
   const int heads = prm.heads[0] + prm.heads[1];
   if (e4m3) {
+    static std::atomic<uint64_t> attr_done{0};
+    const int rc = ensure_smem_attr(rope_e4m3_kernel<D, INTER>, RopeBlock<D>::kSmem, attr_done);
+    if (rc != DIT_OK) return rc;
     const long long blocks = static_cast<long long>(prm.B) * ((prm.S + kRopeBlockRows - 1) / kRopeBlockRows);
-    const int per = rope_heads_per(blocks, heads, 148 * 3);
+    const int per = rope_heads_per(blocks, heads, 148 * 2);
     const dim3 grid(static_cast<unsigned>(blocks), (heads + per - 1) / per);
-    rope_e4m3_kernel<D, INTER><<<grid, kRopeBlockThreads, 0, st>>>(prm, per);
+    rope_e4m3_kernel<D, INTER><<<grid, kRopeThreads, RopeBlock<D>::kSmem, st>>>(prm, per);
   } else {
-    constexpr int kTokens = kRopeThreads * 8 / D;
+    constexpr int kTokens = kRopeThreads * 16 / D;
     const long long blocks = (static_cast<long long>(prm.B) * prm.S + kTokens - 1) / kTokens;
-    const int per = rope_heads_per(blocks, heads, 148 * 8);
+    const int per = rope_heads_per(blocks, heads, 148 * 2);
     const dim3 grid(static_cast<unsigned>(blocks), (heads + per - 1) / per);
     rope_kernel<D, INTER><<<grid, kRopeThreads, 0, st>>>(prm, per);
   }

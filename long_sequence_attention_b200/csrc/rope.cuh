@@ -8,13 +8,15 @@
 // Each pair belongs to one position axis (1 for text, up to 3 for t, y, x grids).
 //
 // Angles in whole turns, 64-bit fixed point: F = freq / 2 pi * 2^64 mod 2^64, and position * F
-// in 64-bit integer arithmetic drops whole turns exactly, so far positions lose nothing; the
-// top 32 bits are the angle in units of 2^-32 turns, and sincospi takes it from there.
+// in 64-bit integer arithmetic drops whole turns exactly, so far positions lose nothing.  Of the
+// fraction the nearest quarter turn comes off in integers too; cosine and sine of the rest, at most an
+// eighth of a turn, are polynomials (fit_rope_poly.py), within 2 * 2^-24 absolutely.
 //
-// Bytes bound: q and k are read once and written once.  Eight elements a lane, 16 (D = 128) or 8 lanes a head
-// row; a lane's eight are four whole pairs in either layout (two runs of four, half the rotated part
-// apart, in the half layout), so nothing crosses lanes but the norm's sum.  A thread keeps its token and walks over
-// heads, so the angles are formed once for many heads.
+// Bytes bound: q and k are read once and written once.  Sixteen elements a lane, D / 16 lanes a head row; a
+// lane's sixteen are eight whole pairs in either layout (two runs of eight, half the rotated part apart, in
+// the half layout), so nothing crosses lanes but the norm's sum, and pairs of pairs go through packed fp32
+// instructions.  Angles are formed once for many heads: a thread keeps its token, or (E4M3) a CTA keeps its
+// block's in shared memory, and walks over heads.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -51,110 +53,169 @@ __device__ __forceinline__ unsigned long long rope_turns(double freq) {
   return f < 1.0 ? __double2ull_rz(f * 18446744073709551616.0) : 0ull;
 }
 
-// cos and sin of position * freq times the magnitude.  The nearest quarter turn is taken off in integers
-// first, so that the rest, at most an eighth of a turn, keeps more of its bits in fp32.
+// cos and sin of position * freq times the magnitude.
 __device__ __forceinline__ void rope_cos_sin(int pos, unsigned long long turns, float magnitude, float& c, float& s) {
   const unsigned long long t = static_cast<unsigned long long>(static_cast<long long>(pos)) * turns;
   const uint32_t hi = static_cast<uint32_t>(t >> 32);           // in 2^-32 turns
   const uint32_t quarter = (hi + 0x20000000u) >> 30;
   const int rest = static_cast<int>(hi - (quarter << 30));      // in [-2^29, 2^29)
-  float cr, sr;
-  sincospif(static_cast<float>(rest) * 4.6566128730773926e-10f, &sr, &cr);   // 2^-31: half turns
-  const float x = (quarter & 1u) ? sr : cr, y = (quarter & 1u) ? cr : sr;
-  c = ((quarter + 1u) & 2u) ? -x * magnitude : x * magnitude;
-  s = (quarter & 2u) ? -y * magnitude : y * magnitude;
+  const float x = static_cast<float>(rest) * 4.6566128730773926e-10f;   // 2^-31: half turns, |x| <= 1/4
+  const float u = x * x;
+  float sp = fmaf(0.08099587261676788f, u, -0.5992013812065125f);
+  sp = fmaf(sp, u, 2.5501625537872314f);
+  sp = fmaf(sp, u, -5.167712688446045f);
+  sp = fmaf(sp, u, 3.1415927410125732f) * x;
+  float cp = fmaf(0.23126092553138733f, u, -1.3350359201431274f);
+  cp = fmaf(cp, u, 4.058706760406494f);
+  cp = fmaf(cp, u, -4.934802055358887f);
+  cp = fmaf(cp, u, 1.0f);
+  const float a = (quarter & 1u) ? sp : cp, b = (quarter & 1u) ? cp : sp;
+  c = ((quarter + 1u) & 2u) ? -a * magnitude : a * magnitude;
+  s = (quarter & 2u) ? -b * magnitude : b * magnitude;
 }
 
-// A lane's part of a head: elements lo .. lo + 3 and hi .. hi + 3; pairs 4 lane .. 4 lane + 3.
+// The turns and the axis of every pair, in shared memory.
+struct RopeTable {
+  unsigned long long turns[64];
+  int axis[64];
+};
+__device__ __forceinline__ void rope_fill(const RopeParams& p, RopeTable& tab) {
+  for (int i = threadIdx.x; i < p.rot / 2; i += blockDim.x) {
+    tab.turns[i] = rope_turns(p.freqs[i]);
+    int axis = 0;
+#pragma unroll
+    for (int a = 0; a + 1 < kMaxRopeAxes; ++a)
+      if (a + 1 < p.axes && i >= p.axis_end[a]) axis = a + 1;
+    tab.axis[i] = axis;
+  }
+  __syncthreads();
+}
+
+// Where a lane's elements lie: a (first of each pair) and b (second).  Inside the half layout's rotated part, a is
+// elements lo .. lo + 7 and b is hi .. hi + 7; else both are interleaved in lo .. lo + 15.
 struct RopeLane {
   int lo, hi;
-  bool split;                    // half layout, inside the rotated part: two 8-byte accesses
-  bool turn[4];                  // pair k is rotated
-  float c[4], s[4];
+  bool split;
+  uint32_t turn;                 // bit k: pair k is rotated
 };
-
-template <int D, bool INTER>
-__device__ __forceinline__ RopeLane rope_lane(const RopeParams& p, int lane, const int* pos, bool on) {
+template <bool INTER>
+__device__ __forceinline__ RopeLane rope_lane(int rot, int lane) {
   RopeLane r;
-  const int pairs = p.rot / 2;
-  r.split = !INTER && lane * 4 < pairs;
-  r.lo = r.split ? 4 * lane : 8 * lane;
-  r.hi = r.split ? 4 * lane + pairs : 8 * lane + 4;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int i = 4 * lane + k;
-    r.turn[k] = i < pairs;
-    r.c[k] = 1.0f;
-    r.s[k] = 0.0f;
-    if (on && r.turn[k]) {
-      int axis = 0;
-#pragma unroll
-      for (int a = 0; a + 1 < kMaxRopeAxes; ++a)
-        if (a + 1 < p.axes && i >= p.axis_end[a]) axis = a + 1;
-      rope_cos_sin(__ldg(pos + axis), rope_turns(__ldg(p.freqs + i)), p.magnitude, r.c[k], r.s[k]);
-    }
-  }
+  const int pairs = rot / 2, left = pairs - 8 * lane;           // pairs 8 lane .. 8 lane + 7
+  r.split = !INTER && left > 0;
+  r.lo = r.split ? 8 * lane : 16 * lane;
+  r.hi = r.split ? 8 * lane + pairs : 16 * lane + 8;
+  r.turn = left >= 8 ? 0xFFu : (left <= 0 ? 0u : (1u << left) - 1u);
   return r;
 }
 
-template <bool INTER>
-__device__ __forceinline__ uint4 rope_load(const __nv_bfloat16* x, const RopeLane& r) {
-  if (INTER) return __ldg(reinterpret_cast<const uint4*>(x + r.lo));
-  const uint2 a = __ldg(reinterpret_cast<const uint2*>(x + r.lo)), b = __ldg(reinterpret_cast<const uint2*>(x + r.hi));
-  return make_uint4(a.x, a.y, b.x, b.y);
+struct RopeRaw { uint4 x, y; };
+__device__ __forceinline__ RopeRaw rope_load(const __nv_bfloat16* x, const RopeLane& r) {
+  return RopeRaw{__ldg(reinterpret_cast<const uint4*>(x + r.lo)), __ldg(reinterpret_cast<const uint4*>(x + r.hi))};
 }
 
-// Norm (where w is given) and rotation of a lane's eight elements.
-template <int D, bool INTER>
-__device__ __forceinline__ void rope_apply(const RopeLane& r, const uint4& raw, bool norm, const float (&w)[8], float eps,
-                                           float (&y)[8]) {
-  float v[8];
-  NormVec<__nv_bfloat16>::unpack(raw, v);
-  if (norm) {
-    float ss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-#pragma unroll
-    for (int o = D / 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float inv = __frsqrt_rn(ss * (1.0f / D) + eps);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = v[i] * inv * w[i];
-  }
+// A lane's pairs as packed fp32: a[k] = first elements of pairs 2k and 2k + 1, b[k] their second ones.
+template <bool INTER>
+__device__ __forceinline__ void rope_unpack(const RopeRaw& raw, uint64_t (&a)[4], uint64_t (&b)[4]) {
+  const uint32_t w[8] = {raw.x.x, raw.x.y, raw.x.z, raw.x.w, raw.y.x, raw.y.y, raw.y.z, raw.y.w};
+  auto lo = [](uint32_t v) { return __uint_as_float(v << 16); };
+  auto hi = [](uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); };
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int ia = INTER ? 2 * k : k, ib = INTER ? 2 * k + 1 : k + 4;
     if (INTER) {
-      const float a = v[ia], b = v[ib];
-      y[ia] = r.turn[k] ? a * r.c[k] - b * r.s[k] : a;
-      y[ib] = r.turn[k] ? b * r.c[k] + a * r.s[k] : b;
+      a[k] = f2_pack(lo(w[2 * k]), lo(w[2 * k + 1]));
+      b[k] = f2_pack(hi(w[2 * k]), hi(w[2 * k + 1]));
     } else {
-      const float a = v[ia], b = v[ib];
-      y[ia] = r.split ? a * r.c[k] - b * r.s[k] : a;
-      y[ib] = r.split ? b * r.c[k] + a * r.s[k] : b;
+      a[k] = f2_pack(lo(w[k]), hi(w[k]));
+      b[k] = f2_pack(lo(w[4 + k]), hi(w[4 + k]));
     }
   }
 }
 
-__device__ __forceinline__ void rope_weights(const __nv_bfloat16* w, const RopeLane& r, float (&v)[8]) {
-  if (w == nullptr) return;
-  const uint2 a = __ldg(reinterpret_cast<const uint2*>(w + r.lo)), b = __ldg(reinterpret_cast<const uint2*>(w + r.hi));
-  NormVec<__nv_bfloat16>::unpack(make_uint4(a.x, a.y, b.x, b.y), v);
+// Norm (where weights are given, as raw) and rotation.
+template <int D, bool INTER>
+__device__ __forceinline__ void rope_apply(const RopeLane& r, const RopeRaw& raw, bool norm, const RopeRaw& weight, float eps,
+                                           const uint64_t (&c)[4], const uint64_t (&s)[4], uint64_t (&ya)[4],
+                                           uint64_t (&yb)[4]) {
+  uint64_t a[4], b[4];
+  rope_unpack<INTER>(raw, a, b);
+  if (norm) {
+    uint64_t q = 0ull;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) q = f2_fma(a[k], a[k], f2_fma(b[k], b[k], q));
+    float q0, q1;
+    f2_unpack(q, q0, q1);
+    float ss = q0 + q1;
+#pragma unroll
+    for (int o = D / 32; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float inv = __frsqrt_rn(ss * (1.0f / D) + eps);
+    const uint64_t inv2 = f2_pack(inv, inv);
+    uint64_t wa[4], wb[4];
+    rope_unpack<INTER>(weight, wa, wb);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      a[k] = f2_mul(f2_mul(a[k], inv2), wa[k]);
+      b[k] = f2_mul(f2_mul(b[k], inv2), wb[k]);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    ya[k] = f2_sub(f2_mul(a[k], c[k]), f2_mul(b[k], s[k]));
+    yb[k] = f2_fma(a[k], s[k], f2_mul(b[k], c[k]));
+  }
+  if (r.turn != 0xFFu) {         // elements past rot pass unchanged
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float a0, a1, b0, b1, y0, y1, z0, z1;
+      f2_unpack(a[k], a0, a1);
+      f2_unpack(b[k], b0, b1);
+      f2_unpack(ya[k], y0, y1);
+      f2_unpack(yb[k], z0, z1);
+      const bool t0 = (r.turn >> (2 * k)) & 1u, t1 = (r.turn >> (2 * k + 1)) & 1u;
+      ya[k] = f2_pack(t0 ? y0 : a0, t1 ? y1 : a1);
+      yb[k] = f2_pack(t0 ? z0 : b0, t1 ? z1 : b1);
+    }
+  }
 }
 
-// bf16 out.  A CTA takes 256 * 8 / D tokens (of all batches, one after another) and heads_per heads of q and k
-// together; four heads' loads are in flight at a time.
+// A lane's angles (0 where nothing turns).
+__device__ __forceinline__ void rope_angles(const RopeParams& p, const RopeTable& tab, const RopeLane& r, int lane, const int* pos,
+                                            bool on, float (&c)[8], float (&s)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    c[k] = s[k] = 0.0f;
+    const int i = 8 * lane + k;
+    if (on && ((r.turn >> k) & 1u)) rope_cos_sin(__ldg(pos + tab.axis[i]), tab.turns[i], p.magnitude, c[k], s[k]);
+  }
+}
+
+// bf16 out.  A CTA takes 256 * 16 / D tokens (of all batches, one after another) and heads_per heads of q and k
+// together, four heads' loads in flight at a time (B200, 40 + 40 heads x 32760 x 128, normed: 221 us, 6.07 TB/s; two
+// heads and three CTAs on an SM 242).
 constexpr int kRopeThreads = 256;
 constexpr int kRopeUnroll = 4;
 
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, int heads_per) {
-  constexpr int kLanes = D / 8;
+__global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const RopeParams p, int heads_per) {
+  constexpr int kLanes = D / 16;
+  __shared__ RopeTable tab;
+  rope_fill(p, tab);
   const long long n = static_cast<long long>(blockIdx.x) * (kRopeThreads / kLanes) + threadIdx.x / kLanes;
   const bool on = n < static_cast<long long>(p.B) * p.S;
   const long long b = on ? n / p.S : 0;
   const int s = on ? static_cast<int>(n - b * p.S) : 0;
   const int lane = threadIdx.x % kLanes;
-  const RopeLane r = rope_lane<D, INTER>(p, lane, p.pos + b * p.pos_sb + static_cast<long long>(s) * p.axes, on);
+  const RopeLane r = rope_lane<INTER>(p.rot, lane);
+  uint64_t c2[4], s2[4];
+  {
+    float c[8], sn[8];
+    rope_angles(p, tab, r, lane, p.pos + b * p.pos_sb + static_cast<long long>(s) * p.axes, on, c, sn);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      c2[k] = f2_pack(c[2 * k], c[2 * k + 1]);
+      s2[k] = f2_pack(sn[2 * k], sn[2 * k + 1]);
+    }
+  }
   const int first = blockIdx.y * heads_per, last = min(first + heads_per, p.heads[0] + p.heads[1]);
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
@@ -162,55 +223,82 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
     const int h0 = max(first - shift, 0), h1 = min(last - shift, p.heads[which]);
     if (h0 >= h1) continue;
     const bool norm = p.weight[which] != nullptr;
-    float w[8];
-    rope_weights(p.weight[which], r, w);
-    const __nv_bfloat16* x = p.x[which] + b * p.sb[which] + s * p.ss[which];
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out[which]) + (b * p.heads[which] * p.S + s) * D;
-    const long long step = static_cast<long long>(p.S) * D;
+    RopeRaw w = {};
+    if (norm) w = rope_load(p.weight[which], r);
+    const long long sh = p.sh[which], step = static_cast<long long>(p.S) * D;
+    const __nv_bfloat16* x = p.x[which] + b * p.sb[which] + s * p.ss[which] + h0 * sh;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out[which]) + ((b * p.heads[which] + h0) * p.S + s) * D;
 #pragma unroll 1
     for (int h = h0; h < h1; h += kRopeUnroll) {
-      uint4 raw[kRopeUnroll];
-#pragma unroll
-      for (int i = 0; i < kRopeUnroll; ++i)
-        raw[i] = on && h + i < h1 ? rope_load<INTER>(x + (h + i) * p.sh[which], r) : make_uint4(0u, 0u, 0u, 0u);
+      RopeRaw raw[kRopeUnroll];
 #pragma unroll
       for (int i = 0; i < kRopeUnroll; ++i) {
-        float y[8];
-        rope_apply<D, INTER>(r, raw[i], norm, w, p.eps, y);
-        if (on && h + i < h1) {
-          const uint4 o = NormVec<__nv_bfloat16>::pack(y);
-          __nv_bfloat16* dst = out + (h + i) * step;
+        raw[i] = RopeRaw{};
+        if (on && h + i < h1) raw[i] = rope_load(x + i * sh, r);
+      }
+#pragma unroll
+      for (int i = 0; i < kRopeUnroll; ++i) {
+        uint64_t ya[4], yb[4];
+        rope_apply<D, INTER>(r, raw[i], norm, w, p.eps, c2, s2, ya, yb);
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float a0, a1, b0, b1;
+          f2_unpack(ya[k], a0, a1);
+          f2_unpack(yb[k], b0, b1);
           if (INTER) {
-            *reinterpret_cast<uint4*>(dst + r.lo) = o;
+            o[2 * k] = pack_bf16x2(a0, b0);
+            o[2 * k + 1] = pack_bf16x2(a1, b1);
           } else {
-            *reinterpret_cast<uint2*>(dst + r.lo) = make_uint2(o.x, o.y);
-            *reinterpret_cast<uint2*>(dst + r.hi) = make_uint2(o.z, o.w);
+            o[k] = pack_bf16x2(a0, a1);
+            o[4 + k] = pack_bf16x2(b0, b1);
           }
         }
+        if (on && h + i < h1) {
+          *reinterpret_cast<uint4*>(out + i * step + r.lo) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(out + i * step + r.hi) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
       }
+      x += kRopeUnroll * sh;
+      out += kRopeUnroll * step;
     }
   }
 }
 
 // E4M3 out.  A CTA takes a block of 128 tokens and heads_per heads, one head at a time: the block stays in
-// registers between its maximum and its codes, and the next head's loads are under way meanwhile.
+// registers between its maximum and its codes, the next head's loads are under way meanwhile, and the block's
+// cosines and sines stay in shared memory (64 KB at D = 128: two CTAs on an SM).
 constexpr int kRopeBlockRows = 128;
-constexpr int kRopeBlockThreads = 512;
+template <int D>
+struct RopeBlock {
+  static constexpr int kLanes = D / 16, kRows = kRopeThreads / kLanes, kPass = kRopeBlockRows / kRows;
+  static constexpr int kSmem = kRopeBlockRows * D / 2 * 8;      // four planes of float4: c, c', s, s' of a lane's pairs
+};
 
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kRopeBlockThreads, 1) rope_e4m3_kernel(const RopeParams p, int heads_per) {
-  constexpr int kLanes = D / 8, kRows = kRopeBlockThreads / kLanes, kPass = kRopeBlockRows / kRows;
-  __shared__ float red[2][kRopeBlockThreads / 32];
+__global__ void __launch_bounds__(kRopeThreads, 2) rope_e4m3_kernel(const RopeParams p, int heads_per) {
+  using R = RopeBlock<D>;
+  constexpr int kLanes = R::kLanes, kRows = R::kRows, kPass = R::kPass, kPlane = kRopeBlockRows * kLanes;
+  extern __shared__ float4 planes[];
+  __shared__ RopeTable tab;
+  __shared__ float red[2][kRopeThreads / 32];
+  rope_fill(p, tab);
   const int nblk = (p.S + kRopeBlockRows - 1) / kRopeBlockRows;
   const long long b = blockIdx.x / nblk;
   const int blk = blockIdx.x % nblk;
-  const int s0 = blk * kRopeBlockRows + threadIdx.x / kLanes;
+  const int row0 = threadIdx.x / kLanes, s0 = blk * kRopeBlockRows + row0;
   const int lane = threadIdx.x % kLanes;
-  RopeLane r[kPass];
-#pragma unroll
+  const RopeLane r = rope_lane<INTER>(p.rot, lane);
+#pragma unroll 1
   for (int i = 0; i < kPass; ++i) {
     const int s = s0 + i * kRows;
-    r[i] = rope_lane<D, INTER>(p, lane, p.pos + b * p.pos_sb + static_cast<long long>(s) * p.axes, s < p.S);
+    float c[8], sn[8];
+    rope_angles(p, tab, r, lane, p.pos + b * p.pos_sb + static_cast<long long>(s) * p.axes, s < p.S, c, sn);
+    const int at = (row0 + i * kRows) * kLanes + lane;            // (read back by the thread that wrote it)
+    planes[at] = make_float4(c[0], c[1], c[2], c[3]);
+    planes[kPlane + at] = make_float4(c[4], c[5], c[6], c[7]);
+    planes[2 * kPlane + at] = make_float4(sn[0], sn[1], sn[2], sn[3]);
+    planes[3 * kPlane + at] = make_float4(sn[4], sn[5], sn[6], sn[7]);
   }
   const int first = blockIdx.y * heads_per, last = min(first + heads_per, p.heads[0] + p.heads[1]);
   int flip = 0;
@@ -220,55 +308,74 @@ __global__ void __launch_bounds__(kRopeBlockThreads, 1) rope_e4m3_kernel(const R
     const int h0 = max(first - shift, 0), h1 = min(last - shift, p.heads[which]);
     if (h0 >= h1) continue;
     const bool norm = p.weight[which] != nullptr;
-    float w[8];
-    rope_weights(p.weight[which], r[0], w);
-    const __nv_bfloat16* x = p.x[which] + b * p.sb[which] + s0 * p.ss[which];
-    const long long step = kRows * p.ss[which];
-    uint4 raw[kPass];
-    auto load = [&](int h) {
+    RopeRaw w = {};
+    if (norm) w = rope_load(p.weight[which], r);
+    const long long sh = p.sh[which], step = kRows * p.ss[which];
+    const __nv_bfloat16* x = p.x[which] + b * p.sb[which] + s0 * p.ss[which] + h0 * sh;
+    RopeRaw raw[kPass];
 #pragma unroll
-      for (int i = 0; i < kPass; ++i)
-        raw[i] = s0 + i * kRows < p.S ? rope_load<INTER>(x + h * p.sh[which] + i * step, r[i]) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    load(h0);
+    for (int i = 0; i < kPass; ++i) {
+      raw[i] = RopeRaw{};
+      if (s0 + i * kRows < p.S) raw[i] = rope_load(x + i * step, r);
+    }
 #pragma unroll 1
     for (int h = h0; h < h1; ++h) {
-      float y[kPass][8];
+      uint64_t ya[kPass][4], yb[kPass][4];
       float m = 0.0f;
+      x += sh;
 #pragma unroll
       for (int i = 0; i < kPass; ++i) {
-        rope_apply<D, INTER>(r[i], raw[i], norm, w, p.eps, y[i]);
+        const int at = (row0 + i * kRows) * kLanes + lane;
+        const float4 ca = planes[at], cb = planes[kPlane + at], sa = planes[2 * kPlane + at], sb = planes[3 * kPlane + at];
+        const uint64_t c2[4] = {f2_pack(ca.x, ca.y), f2_pack(ca.z, ca.w), f2_pack(cb.x, cb.y), f2_pack(cb.z, cb.w)};
+        const uint64_t s2[4] = {f2_pack(sa.x, sa.y), f2_pack(sa.z, sa.w), f2_pack(sb.x, sb.y), f2_pack(sb.z, sb.w)};
+        rope_apply<D, INTER>(r, raw[i], norm, w, p.eps, c2, s2, ya[i], yb[i]);
+        if (h + 1 < h1 && s0 + i * kRows < p.S) raw[i] = rope_load(x + i * step, r);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[i][e]));
+        for (int k = 0; k < 4; ++k) {
+          float a0, a1, b0, b1;
+          f2_unpack(ya[i][k], a0, a1);
+          f2_unpack(yb[i][k], b0, b1);
+          m = fmax3(m, fabsf(a0), fabsf(a1));
+          m = fmax3(m, fabsf(b0), fabsf(b1));
+        }
       }
-      if (h + 1 < h1) load(h + 1);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       if ((threadIdx.x & 31) == 0) red[flip][threadIdx.x >> 5] = m;
       __syncthreads();
-      m = red[flip][threadIdx.x & (kRopeBlockThreads / 32 - 1)];
+      m = red[flip][threadIdx.x & (kRopeThreads / 32 - 1)];
 #pragma unroll
-      for (int o = kRopeBlockThreads / 64; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int o = kRopeThreads / 64; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       flip ^= 1;                                  // (two buffers: one barrier a head is enough)
       const float d = m > 0.0f ? __fdiv_rn(m, 448.0f) : 1.0f;
       const float rcp = __frcp_rn(d);
       const long long bh = b * p.heads[which] + h;
       if (threadIdx.x == 0) p.descales[which][bh * nblk + blk] = m > 0.0f ? d : 0.0f;
       uint8_t* out = static_cast<uint8_t*>(p.out[which]) + (bh * p.S + s0) * D;
+      const uint64_t rcp2 = f2_pack(rcp, rcp);
 #pragma unroll
       for (int i = 0; i < kPass; ++i) {
-        if (s0 + i * kRows >= p.S) break;
-        uint32_t c[2];
+        uint32_t c[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          c[e] = pack_e4m3x4(quot_e4m3(y[i][4 * e], d, rcp), quot_e4m3(y[i][4 * e + 1], d, rcp),
-                             quot_e4m3(y[i][4 * e + 2], d, rcp), quot_e4m3(y[i][4 * e + 3], d, rcp));
-        uint8_t* dst = out + static_cast<long long>(i) * kRows * D;
-        if (INTER) {
-          *reinterpret_cast<uint2*>(dst + r[i].lo) = make_uint2(c[0], c[1]);
-        } else {
-          *reinterpret_cast<uint32_t*>(dst + r[i].lo) = c[0];
-          *reinterpret_cast<uint32_t*>(dst + r[i].hi) = c[1];
+        for (int k = 0; k < 2; ++k) {
+          float a0, a1, a2, a3, b0, b1, b2, b3;
+          f2_unpack(f2_mul(ya[i][2 * k], rcp2), a0, a1);
+          f2_unpack(f2_mul(ya[i][2 * k + 1], rcp2), a2, a3);
+          f2_unpack(f2_mul(yb[i][2 * k], rcp2), b0, b1);
+          f2_unpack(f2_mul(yb[i][2 * k + 1], rcp2), b2, b3);
+          if (INTER) {
+            c[2 * k] = pack_e4m3x4(a0, b0, a1, b1);
+            c[2 * k + 1] = pack_e4m3x4(a2, b2, a3, b3);
+          } else {
+            c[k] = pack_e4m3x4(a0, a1, a2, a3);
+            c[2 + k] = pack_e4m3x4(b0, b1, b2, b3);
+          }
+        }
+        if (s0 + i * kRows < p.S) {
+          uint8_t* dst = out + static_cast<long long>(i) * kRows * D;
+          *reinterpret_cast<uint2*>(dst + r.lo) = make_uint2(c[0], c[1]);
+          *reinterpret_cast<uint2*>(dst + r.hi) = make_uint2(c[2], c[3]);
         }
       }
     }
