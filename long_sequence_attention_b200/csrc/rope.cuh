@@ -13,9 +13,8 @@
 // eighth of a turn, are polynomials (fit_rope_poly.py), within 2 * 2^-24 absolutely.
 //
 // Bytes bound: q and k are read once and written once.  Sixteen elements a lane, D / 16 lanes a head row; a
-// lane's sixteen are eight whole pairs in either layout (two runs of eight, half the rotated part apart, in
-// the half layout), so nothing crosses lanes but the norm's sum, and pairs of pairs go through packed fp32
-// instructions.  Angles are formed once for many heads: a thread keeps its token, or (E4M3) a CTA keeps its
+// lane's sixteen are two runs of eight and hold eight whole pairs in either layout, so nothing crosses lanes but
+// the norm's sum, and pairs of pairs go through packed fp32 instructions.  Angles are formed once for many heads: a thread keeps its token, or (E4M3) a CTA keeps its
 // block's in shared memory, and walks over heads.
 #pragma once
 
@@ -91,21 +90,26 @@ __device__ __forceinline__ void rope_fill(const RopeParams& p, RopeTable& tab) {
   __syncthreads();
 }
 
-// Where a lane's elements lie: a (first of each pair) and b (second).  Inside the half layout's rotated part, a is
-// elements lo .. lo + 7 and b is hi .. hi + 7; else both are interleaved in lo .. lo + 15.
+// Where a lane's elements lie: two runs of eight, lo .. and hi .., neighbouring lanes next to each other.  Interleaved:
+// four pairs in each.  Half layout, inside the rotated part: the first elements of eight pairs and their second ones.
+// `first` and `second` are the pairs that the runs' four (interleaved) or the lane's eight (half) begin with.
 struct RopeLane {
-  int lo, hi;
-  bool split;
-  uint32_t turn;                 // bit k: pair k is rotated
+  int lo, hi, first, second;
+  uint32_t turn;                 // bit k: the lane's pair k is rotated
 };
-template <bool INTER>
+template <int D, bool INTER>
 __device__ __forceinline__ RopeLane rope_lane(int rot, int lane) {
   RopeLane r;
-  const int pairs = rot / 2, left = pairs - 8 * lane;           // pairs 8 lane .. 8 lane + 7
-  r.split = !INTER && left > 0;
-  r.lo = r.split ? 8 * lane : 16 * lane;
-  r.hi = r.split ? 8 * lane + pairs : 16 * lane + 8;
-  r.turn = left >= 8 ? 0xFFu : (left <= 0 ? 0u : (1u << left) - 1u);
+  const int pairs = rot / 2;
+  const bool split = !INTER && 8 * lane < pairs;
+  r.lo = split || INTER ? 8 * lane : 16 * lane;
+  r.hi = split ? 8 * lane + pairs : (INTER ? D / 2 + 8 * lane : 16 * lane + 8);
+  r.first = INTER ? 4 * lane : 8 * lane;
+  r.second = INTER ? D / 4 + 4 * lane : 8 * lane + 4;
+  r.turn = 0u;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if ((k < 4 ? r.first + k : r.second + k - 4) < pairs) r.turn |= 1u << k;
   return r;
 }
 
@@ -114,7 +118,7 @@ __device__ __forceinline__ RopeRaw rope_load(const __nv_bfloat16* x, const RopeL
   return RopeRaw{__ldg(reinterpret_cast<const uint4*>(x + r.lo)), __ldg(reinterpret_cast<const uint4*>(x + r.hi))};
 }
 
-// A lane's pairs as packed fp32: a[k] = first elements of pairs 2k and 2k + 1, b[k] their second ones.
+// A lane's pairs as packed fp32: a[k] = first elements of its pairs 2k and 2k + 1, b[k] their second ones.
 template <bool INTER>
 __device__ __forceinline__ void rope_unpack(const RopeRaw& raw, uint64_t (&a)[4], uint64_t (&b)[4]) {
   const uint32_t w[8] = {raw.x.x, raw.x.y, raw.x.z, raw.x.w, raw.y.x, raw.y.y, raw.y.z, raw.y.w};
@@ -179,12 +183,12 @@ __device__ __forceinline__ void rope_apply(const RopeLane& r, const RopeRaw& raw
 }
 
 // A lane's angles (0 where nothing turns).
-__device__ __forceinline__ void rope_angles(const RopeParams& p, const RopeTable& tab, const RopeLane& r, int lane, const int* pos,
-                                            bool on, float (&c)[8], float (&s)[8]) {
+__device__ __forceinline__ void rope_angles(const RopeParams& p, const RopeTable& tab, const RopeLane& r, const int* pos, bool on,
+                                            float (&c)[8], float (&s)[8]) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     c[k] = s[k] = 0.0f;
-    const int i = 8 * lane + k;
+    const int i = k < 4 ? r.first + k : r.second + k - 4;
     if (on && ((r.turn >> k) & 1u)) rope_cos_sin(__ldg(pos + tab.axis[i]), tab.turns[i], p.magnitude, c[k], s[k]);
   }
 }
@@ -205,11 +209,11 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const RopeParams 
   const long long b = on ? n / p.S : 0;
   const int s = on ? static_cast<int>(n - b * p.S) : 0;
   const int lane = threadIdx.x % kLanes;
-  const RopeLane r = rope_lane<INTER>(p.rot, lane);
+  const RopeLane r = rope_lane<D, INTER>(p.rot, lane);
   uint64_t c2[4], s2[4];
   {
     float c[8], sn[8];
-    rope_angles(p, tab, r, lane, p.pos + b * p.pos_sb + static_cast<long long>(s) * p.axes, on, c, sn);
+    rope_angles(p, tab, r, p.pos + b * p.pos_sb + static_cast<long long>(s) * p.axes, on, c, sn);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       c2[k] = f2_pack(c[2 * k], c[2 * k + 1]);
@@ -265,121 +269,145 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const RopeParams 
   }
 }
 
-// E4M3 out.  A CTA takes a block of 128 tokens and heads_per heads, one head at a time: the block stays in
-// registers between its maximum and its codes, the next head's loads are under way meanwhile, and the block's
-// cosines and sines stay in shared memory (64 KB at D = 128: two CTAs on an SM).
+// E4M3 out.  A CTA takes a block of 128 tokens and heads_per heads.  Its two halves of 256 threads take one head
+// each at a time: the block stays in registers between its maximum and its codes.  Both share the block's cosines and
+// sines in shared memory (64 KB at D = 128), and each has the next two heads' loads under way into shared memory
+// (asynchronous copies that only the thread that made them reads back, so that they need no barrier).
 constexpr int kRopeBlockRows = 128;
+constexpr int kRopeStages = 2;
 template <int D>
 struct RopeBlock {
   static constexpr int kLanes = D / 16, kRows = kRopeThreads / kLanes, kPass = kRopeBlockRows / kRows;
-  static constexpr int kSmem = kRopeBlockRows * D / 2 * 8;      // four planes of float4: c, c', s, s' of a lane's pairs
+  static constexpr int kPlanes = kRopeBlockRows * D / 2 * 8;    // four planes of float4: c, c', s, s' of a lane's pairs
+  static constexpr int kStage = kRopeBlockRows * D * 2;
+  static constexpr int kSmem = kPlanes + 2 * kRopeStages * kStage;   // 192 KB, D = 64: 96 KB
+  static constexpr int kCtas = 1;                               // on an SM (registers: 512 threads of 128)
 };
 
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, 2) rope_e4m3_kernel(const RopeParams p, int heads_per) {
+__global__ void __launch_bounds__(2 * kRopeThreads, 1) rope_e4m3_kernel(const RopeParams p, int heads_per) {
   using R = RopeBlock<D>;
   constexpr int kLanes = R::kLanes, kRows = R::kRows, kPass = R::kPass, kPlane = kRopeBlockRows * kLanes;
   extern __shared__ float4 planes[];
   __shared__ RopeTable tab;
-  __shared__ float red[2][kRopeThreads / 32];
+  __shared__ float red[2][2][kRopeThreads / 32];
   rope_fill(p, tab);
+  const int half = threadIdx.x / kRopeThreads, tid = threadIdx.x % kRopeThreads;
   const int nblk = (p.S + kRopeBlockRows - 1) / kRopeBlockRows;
   const long long b = blockIdx.x / nblk;
   const int blk = blockIdx.x % nblk;
-  const int row0 = threadIdx.x / kLanes, s0 = blk * kRopeBlockRows + row0;
-  const int lane = threadIdx.x % kLanes;
-  const RopeLane r = rope_lane<INTER>(p.rot, lane);
+  const int row0 = tid / kLanes, s0 = blk * kRopeBlockRows + row0;
+  const int lane = tid % kLanes;
+  const RopeLane r = rope_lane<D, INTER>(p.rot, lane);
+  const int first = blockIdx.y * heads_per, last = min(first + heads_per, p.heads[0] + p.heads[1]);
+  uint4* stage = reinterpret_cast<uint4*>(planes + R::kPlanes / 16) + half * kRopeStages * (R::kStage / 16) + tid;
+  // loads of this half's k-th head into stage k % kRopeStages: piece e of pass i at (2 i + e) * 256 + tid
+  auto load = [&](int k) {
+    const int hh = first + half + 2 * k;
+    if (hh < last) {
+      const int which = hh >= p.heads[0];
+      const __nv_bfloat16* x = p.x[which] + b * p.sb[which] + s0 * p.ss[which] + (which ? hh - p.heads[0] : hh) * p.sh[which];
+      uint4* dst = stage + (k % kRopeStages) * (R::kStage / 16);
+#pragma unroll
+      for (int i = 0; i < kPass; ++i)
+        if (s0 + i * kRows < p.S) {
+          copy_async16(dst + (2 * i) * kRopeThreads, x + i * kRows * p.ss[which] + r.lo);
+          copy_async16(dst + (2 * i + 1) * kRopeThreads, x + i * kRows * p.ss[which] + r.hi);
+        }
+    }
+    copy_async_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < kRopeStages; ++k) load(k);
 #pragma unroll 1
-  for (int i = 0; i < kPass; ++i) {
+  for (int i = half; i < kPass; i += 2) {
     const int s = s0 + i * kRows;
     float c[8], sn[8];
-    rope_angles(p, tab, r, lane, p.pos + b * p.pos_sb + static_cast<long long>(s) * p.axes, s < p.S, c, sn);
-    const int at = (row0 + i * kRows) * kLanes + lane;            // (read back by the thread that wrote it)
+    rope_angles(p, tab, r, p.pos + b * p.pos_sb + static_cast<long long>(s) * p.axes, s < p.S, c, sn);
+    const int at = (row0 + i * kRows) * kLanes + lane;
     planes[at] = make_float4(c[0], c[1], c[2], c[3]);
     planes[kPlane + at] = make_float4(c[4], c[5], c[6], c[7]);
     planes[2 * kPlane + at] = make_float4(sn[0], sn[1], sn[2], sn[3]);
     planes[3 * kPlane + at] = make_float4(sn[4], sn[5], sn[6], sn[7]);
   }
-  const int first = blockIdx.y * heads_per, last = min(first + heads_per, p.heads[0] + p.heads[1]);
-  int flip = 0;
+  __syncthreads();
+  int at_which = -1;
+  RopeRaw w = {};
 #pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    const int shift = which ? p.heads[0] : 0;
-    const int h0 = max(first - shift, 0), h1 = min(last - shift, p.heads[which]);
-    if (h0 >= h1) continue;
+  for (int k = 0; first + half + 2 * k < last; ++k) {
+    const int hh = first + half + 2 * k, which = hh >= p.heads[0], h = which ? hh - p.heads[0] : hh;
     const bool norm = p.weight[which] != nullptr;
-    RopeRaw w = {};
-    if (norm) w = rope_load(p.weight[which], r);
-    const long long sh = p.sh[which], step = kRows * p.ss[which];
-    const __nv_bfloat16* x = p.x[which] + b * p.sb[which] + s0 * p.ss[which] + h0 * sh;
-    RopeRaw raw[kPass];
+    if (norm && which != at_which) w = rope_load(p.weight[which], r);
+    at_which = which;
+    copy_async_wait<kRopeStages - 1>();
+    const uint4* src = stage + (k % kRopeStages) * (R::kStage / 16);
+    uint64_t ya[kPass][4], yb[kPass][4];
+    float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < kPass; ++i) {
-      raw[i] = RopeRaw{};
-      if (s0 + i * kRows < p.S) raw[i] = rope_load(x + i * step, r);
+      RopeRaw raw = {};
+      if (s0 + i * kRows < p.S) raw = RopeRaw{src[(2 * i) * kRopeThreads], src[(2 * i + 1) * kRopeThreads]};
+      const int at = (row0 + i * kRows) * kLanes + lane;
+      const float4 ca = planes[at], cb = planes[kPlane + at], sa = planes[2 * kPlane + at], sb = planes[3 * kPlane + at];
+      const uint64_t c2[4] = {f2_pack(ca.x, ca.y), f2_pack(ca.z, ca.w), f2_pack(cb.x, cb.y), f2_pack(cb.z, cb.w)};
+      const uint64_t s2[4] = {f2_pack(sa.x, sa.y), f2_pack(sa.z, sa.w), f2_pack(sb.x, sb.y), f2_pack(sb.z, sb.w)};
+      rope_apply<D, INTER>(r, raw, norm, w, p.eps, c2, s2, ya[i], yb[i]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float a0, a1, b0, b1;
+        f2_unpack(ya[i][q], a0, a1);
+        f2_unpack(yb[i][q], b0, b1);
+        m = fmax3(m, fabsf(a0), fabsf(a1));
+        m = fmax3(m, fabsf(b0), fabsf(b1));
+      }
     }
-#pragma unroll 1
-    for (int h = h0; h < h1; ++h) {
-      uint64_t ya[kPass][4], yb[kPass][4];
-      float m = 0.0f;
-      x += sh;
+    load(k + kRopeStages);
 #pragma unroll
-      for (int i = 0; i < kPass; ++i) {
-        const int at = (row0 + i * kRows) * kLanes + lane;
-        const float4 ca = planes[at], cb = planes[kPlane + at], sa = planes[2 * kPlane + at], sb = planes[3 * kPlane + at];
-        const uint64_t c2[4] = {f2_pack(ca.x, ca.y), f2_pack(ca.z, ca.w), f2_pack(cb.x, cb.y), f2_pack(cb.z, cb.w)};
-        const uint64_t s2[4] = {f2_pack(sa.x, sa.y), f2_pack(sa.z, sa.w), f2_pack(sb.x, sb.y), f2_pack(sb.z, sb.w)};
-        rope_apply<D, INTER>(r, raw[i], norm, w, p.eps, c2, s2, ya[i], yb[i]);
-        if (h + 1 < h1 && s0 + i * kRows < p.S) raw[i] = rope_load(x + i * step, r);
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((tid & 31) == 0) red[half][k & 1][tid >> 5] = m;
+    asm volatile("bar.sync %0, %1;" ::"r"(half + 1), "n"(kRopeThreads) : "memory");   // (this half's threads)
+    m = red[half][k & 1][tid & (kRopeThreads / 32 - 1)];       // (two buffers: one barrier a head is enough)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float a0, a1, b0, b1;
-          f2_unpack(ya[i][k], a0, a1);
-          f2_unpack(yb[i][k], b0, b1);
-          m = fmax3(m, fabsf(a0), fabsf(a1));
-          m = fmax3(m, fabsf(b0), fabsf(b1));
+    for (int o = kRopeThreads / 64; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float d = m > 0.0f ? __fdiv_rn(m, 448.0f) : 1.0f;
+    const float rcp = __frcp_rn(d);
+    const long long bh = b * p.heads[which] + h;
+    if (tid == 0) p.descales[which][bh * nblk + blk] = m > 0.0f ? d : 0.0f;
+    uint8_t* out = static_cast<uint8_t*>(p.out[which]) + (bh * p.S + s0) * D;
+    const uint64_t rcp2 = f2_pack(rcp, rcp);
+#pragma unroll
+    for (int i = 0; i < kPass; ++i) {
+      uint32_t c[4];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float a0, a1, a2, a3, b0, b1, b2, b3;
+        f2_unpack(f2_mul(ya[i][2 * q], rcp2), a0, a1);
+        f2_unpack(f2_mul(ya[i][2 * q + 1], rcp2), a2, a3);
+        f2_unpack(f2_mul(yb[i][2 * q], rcp2), b0, b1);
+        f2_unpack(f2_mul(yb[i][2 * q + 1], rcp2), b2, b3);
+        if (INTER) {
+          c[2 * q] = pack_e4m3x4(a0, b0, a1, b1);
+          c[2 * q + 1] = pack_e4m3x4(a2, b2, a3, b3);
+        } else {
+          c[q] = pack_e4m3x4(a0, a1, a2, a3);
+          c[2 + q] = pack_e4m3x4(b0, b1, b2, b3);
         }
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if ((threadIdx.x & 31) == 0) red[flip][threadIdx.x >> 5] = m;
-      __syncthreads();
-      m = red[flip][threadIdx.x & (kRopeThreads / 32 - 1)];
-#pragma unroll
-      for (int o = kRopeThreads / 64; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      flip ^= 1;                                  // (two buffers: one barrier a head is enough)
-      const float d = m > 0.0f ? __fdiv_rn(m, 448.0f) : 1.0f;
-      const float rcp = __frcp_rn(d);
-      const long long bh = b * p.heads[which] + h;
-      if (threadIdx.x == 0) p.descales[which][bh * nblk + blk] = m > 0.0f ? d : 0.0f;
-      uint8_t* out = static_cast<uint8_t*>(p.out[which]) + (bh * p.S + s0) * D;
-      const uint64_t rcp2 = f2_pack(rcp, rcp);
-#pragma unroll
-      for (int i = 0; i < kPass; ++i) {
-        uint32_t c[4];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float a0, a1, a2, a3, b0, b1, b2, b3;
-          f2_unpack(f2_mul(ya[i][2 * k], rcp2), a0, a1);
-          f2_unpack(f2_mul(ya[i][2 * k + 1], rcp2), a2, a3);
-          f2_unpack(f2_mul(yb[i][2 * k], rcp2), b0, b1);
-          f2_unpack(f2_mul(yb[i][2 * k + 1], rcp2), b2, b3);
-          if (INTER) {
-            c[2 * k] = pack_e4m3x4(a0, b0, a1, b1);
-            c[2 * k + 1] = pack_e4m3x4(a2, b2, a3, b3);
-          } else {
-            c[k] = pack_e4m3x4(a0, a1, a2, a3);
-            c[2 + k] = pack_e4m3x4(b0, b1, b2, b3);
-          }
-        }
-        if (s0 + i * kRows < p.S) {
-          uint8_t* dst = out + static_cast<long long>(i) * kRows * D;
-          *reinterpret_cast<uint2*>(dst + r.lo) = make_uint2(c[0], c[1]);
-          *reinterpret_cast<uint2*>(dst + r.hi) = make_uint2(c[2], c[3]);
-        }
+      if (s0 + i * kRows < p.S) {
+        uint8_t* dst = out + static_cast<long long>(i) * kRows * D;
+        *reinterpret_cast<uint2*>(dst + r.lo) = make_uint2(c[0], c[1]);
+        *reinterpret_cast<uint2*>(dst + r.hi) = make_uint2(c[2], c[3]);
       }
     }
   }
+  copy_async_wait<0>();
 }
 
 }  // namespace dit
