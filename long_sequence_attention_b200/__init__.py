@@ -425,14 +425,13 @@ class _Place:
             c.__exit__(*exc)
 
 
-def _elsewhere(device, stream) -> bool:
+def _raw_stream(index: int) -> int:
+    """Address of a device's current stream (what torch.cuda.current_stream holds, without the object)."""
     import torch
-    return stream is not None or device.index != torch.cuda.current_device()
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _raw_stream(device) -> int:
-    import torch
-    return torch._C._cuda_getCurrentRawStream(device.index)
+_ll3, _i3 = ctypes.c_longlong * 3, ctypes.c_int * 3
 
 
 def _need(ok: bool, what: str) -> None:
@@ -462,35 +461,43 @@ def rms_norm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None, g
     E4M3 codes with fp32 descales [..., 1], or [..., ceil(C/128)] with group = 128 (else descales is None).
     stream: h in x's type, written over residual where inplace is true; None without a residual."""
     import torch
-    dt, shape = x.dtype, x.shape
-    bf16 = dt == torch.bfloat16
-    if not (x.is_cuda and (bf16 or dt == torch.float32) and shape and shape[-1]):
+    dt, dev, shape = x.dtype, x.device, x.shape
+    bf16 = dt is torch.bfloat16
+    if not (dev.type == "cuda" and (bf16 or dt is torch.float32) and shape and shape[-1]):
         raise ValueError("x: a CUDA tensor of bf16 or fp32")
-    dev = x.device
-    if _elsewhere(dev, stream):
+    if stream is not None or dev.index != torch.cuda.current_device():
         with _Place(dev, stream):
             return rms_norm(x, weight, residual, eps, out_dtype, group, inplace)
     C = ldx = shape[-1]
-    if not x.is_contiguous():
+    dense = x.is_contiguous()
+    if not dense:
         _need(len(shape) == 2 and x.stride(1) == 1 and x.stride(0) >= C,
               "x: a contiguous tensor, or a matrix whose rows are dense")
         ldx = x.stride(0)
+    wp = rp = hp = dp = h = ds = None
     if weight is not None:
         _like(weight, "weight", dt, (C,), dev)
-    h = None
+        wp = weight.data_ptr()
     if residual is not None:
         _like(residual, "residual", dt, shape, dev)
+        rp = residual.data_ptr()
         h = residual if inplace else torch.empty_like(residual)
+        hp = h.data_ptr()
     elif inplace:
         raise ValueError("inplace needs a residual")
-    code = (DIT_BF16 if bf16 else DIT_FP32) if out_dtype is None else _out_code(out_dtype)
-    out = torch.empty(shape, dtype=dt if out_dtype is None else out_dtype, device=dev)
-    ds = None
-    if code == DIT_FP8_E4M3:
-        ds = torch.empty((*shape[:-1], (C + 127) // 128 if group else 1), dtype=torch.float32, device=dev)
-    _check(lib.dit_rms_norm(x.data_ptr(), ldx, _ptr(residual), _ptr(weight), out.data_ptr(), _ptr(h), _ptr(ds),
-                            x.numel() // C, C, eps, DIT_BF16 if bf16 else DIT_FP32, code, group, _raw_stream(dev)),
-           "dit_rms_norm")
+    if out_dtype is None or out_dtype is dt:
+        code = DIT_BF16 if bf16 else DIT_FP32
+        out = torch.empty_like(x) if dense else x.new_empty(shape)
+    else:
+        code = _out_code(out_dtype)
+        out = x.new_empty(shape, dtype=out_dtype)
+        if code == DIT_FP8_E4M3:
+            ds = x.new_empty((*shape[:-1], (C + 127) // 128 if group else 1), dtype=torch.float32)
+            dp = ds.data_ptr()
+    rc = lib.dit_rms_norm(x.data_ptr(), ldx, rp, wp, out.data_ptr(), hp, dp, x.numel() // C, C, eps,
+                          DIT_BF16 if bf16 else DIT_FP32, code, group, _raw_stream(dev.index))
+    if rc:
+        raise DitError(rc, "dit_rms_norm")
     return out, h, ds
 
 
@@ -544,41 +551,56 @@ def rope_qk(q, k, pos, freqs, q_weight=None, k_weight=None, eps: float = 1e-6, a
     and their descales dq, dk, as attention_fp8_blocks takes them (otherwise dq and dk are None)."""
     import torch
     bf16 = torch.bfloat16
-    _need(q.is_cuda and q.dim() == 4 and q.dtype == bf16, "q: a CUDA bf16 tensor [B, S, H, D]")
-    dev = q.device
-    if _elsewhere(dev, stream):
+    dev, shape = q.device, q.shape
+    if not (dev.type == "cuda" and len(shape) == 4 and q.dtype is bf16):
+        raise ValueError("q: a CUDA bf16 tensor [B, S, H, D]")
+    if stream is not None or dev.index != torch.cuda.current_device():
         with _Place(dev, stream):
             return rope_qk(q, k, pos, freqs, q_weight, k_weight, eps, axis_pairs, interleaved, magnitude, out_dtype)
-    B, S, H, D = q.shape
-    qs, ks, H_kv = q.stride(), None, 0
-    _need(qs[3] == 1, "q: dense heads (stride 1 along D)")
+    B, S, H, D = shape
+    qs, ks, H_kv, kp = q.stride(), (0, 0, 0, 1), 0, None
     if k is not None:
-        H_kv, ks = k.shape[2] if k.dim() == 4 else 0, k.stride()
-        _need(k.dtype == bf16 and k.device == dev and k.shape == (B, S, H_kv, D) and ks[3] == 1,
-              "k: a bf16 tensor [B, S, H_kv, D] on q's device, with dense heads")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _like(w, name, bf16, (D,), dev)
-    ps = pos.shape
+        H_kv, ks, kp = k.shape[2] if k.dim() == 4 else 0, k.stride(), k.data_ptr()
+        _need(k.dtype is bf16 and k.device == dev and k.shape == (B, S, H_kv, D),
+              "k: a bf16 tensor [B, S, H_kv, D] on q's device")
+    _need(qs[3] == 1 and ks[3] == 1, "q, k: dense heads (stride 1 along D)")
+    qw = kw = None
+    if q_weight is not None:
+        _like(q_weight, "q_weight", bf16, (D,), dev)
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        _like(k_weight, "k_weight", bf16, (D,), dev)
+        kw = k_weight.data_ptr()
+    ps, fs = pos.shape, freqs.shape
     axes = ps[2] if len(ps) == 3 else 1
-    _need(pos.dtype == torch.int32 and pos.device == dev and len(ps) in (2, 3) and (ps[0] == B or ps[0] == 1)
-          and ps[1] == S and pos.is_contiguous(), "pos: contiguous int32 [B or 1, S, axes] on q's device")
-    _need(freqs.dtype == torch.float64 and freqs.device == dev and freqs.dim() == 1 and freqs.is_contiguous(),
-          "freqs: a contiguous fp64 vector on q's device")
-    pairs = freqs.shape[0]
+    if not (pos.dtype is torch.int32 and pos.device == dev and len(ps) in (2, 3) and (ps[0] == B or ps[0] == 1)
+            and ps[1] == S and pos.is_contiguous()):
+        raise ValueError("pos: contiguous int32 [B or 1, S, axes] on q's device")
+    if not (freqs.dtype is torch.float64 and freqs.device == dev and len(fs) == 1 and freqs.is_contiguous()):
+        raise ValueError("freqs: a contiguous fp64 vector on q's device")
+    pairs = fs[0]
     per = (pairs,) if axis_pairs is None else axis_pairs
-    _need(len(per) == axes, "axis_pairs: one count for each axis of pos")
-    out_dtype = bf16 if out_dtype is None else out_dtype
+    _need(len(per) == axes and axes <= 3, "axis_pairs: one count for each axis of pos, at most three")
+    if out_dtype is None:
+        out_dtype = bf16
     code = _out_code(out_dtype)
-    q_out = torch.empty((B, H, S, D), dtype=out_dtype, device=dev)
-    k_out = None if k is None else torch.empty((B, H_kv, S, D), dtype=out_dtype, device=dev)
-    dq = dk = None
+    q_out = q.new_empty((B, H, S, D), dtype=out_dtype)
+    k_out = dq = dk = kop = dqp = dkp = None
+    if k is not None:
+        k_out = q.new_empty((B, H_kv, S, D), dtype=out_dtype)
+        kop = k_out.data_ptr()
     if code == DIT_FP8_E4M3:
-        dq = torch.empty((B, H, (S + 127) // 128), dtype=torch.float32, device=dev)
-        dk = None if k is None else torch.empty((B, H_kv, (S + 127) // 128), dtype=torch.float32, device=dev)
-    dit_rope_qk(q, k, qs[:3], None if k is None else ks[:3], q_weight, k_weight, eps, pos,
-                S * axes if ps[0] == B and B > 1 else 0, freqs, per, 2 * pairs, interleaved, magnitude, q_out, k_out,
-                dq, dk, B, S, H, H_kv, D, code, _raw_stream(dev))
+        dq = q.new_empty((B, H, (S + 127) // 128), dtype=torch.float32)
+        dqp = dq.data_ptr()
+        if k is not None:
+            dk = q.new_empty((B, H_kv, (S + 127) // 128), dtype=torch.float32)
+            dkp = dk.data_ptr()
+    rc = lib.dit_rope_qk(q.data_ptr(), kp, _ll3(*qs[:3]), None if k is None else _ll3(*ks[:3]), qw, kw, eps, pos.data_ptr(),
+                         S * axes if B > 1 and ps[0] == B else 0, freqs.data_ptr(), (_i3)(*per), axes, 2 * pairs,
+                         1 if interleaved else 0, magnitude, q_out.data_ptr(), kop, dqp, dkp, B, S, H, H_kv, D, code,
+                         _raw_stream(dev.index))
+    if rc:
+        raise DitError(rc, "dit_rope_qk")
     return q_out, k_out, dq, dk
 
 
@@ -590,29 +612,45 @@ def masked_attention(q, k, v, scale: Optional[float] = None, softcap: float = 0.
     q [B, H, S_q, D], k and v [B, H_kv, S_kv, D] bf16 with H a multiple of H_kv.  q_start int32 [B]: position of each
     sequence's first query among the keys (S_kv - S_q unless given)."""
     import torch
-    bf16, i32 = torch.bfloat16, torch.int32
-    B, H, S_q, D = _dims(q)
-    _need(q.is_cuda and k.dim() == 4, "q, k: CUDA tensors [B, H, S_q, D] and [B, H_kv, S_kv, D]")
-    dev = q.device
-    if _elsewhere(dev, stream):
+    bf16 = torch.bfloat16
+    dev, shape, kshape = q.device, q.shape, k.shape
+    if not (dev.type == "cuda" and len(shape) == 4 and len(kshape) == 4):
+        raise ValueError("q, k: CUDA tensors [B, H, S_q, D] and [B, H_kv, S_kv, D]")
+    if stream is not None or dev.index != torch.cuda.current_device():
         with _Place(dev, stream):
             return masked_attention(q, k, v, scale, softcap, slopes, causal, q_start, prefix, q_doc, kv_doc, with_lse)
-    H_kv, S_kv = k.shape[1], k.shape[2]
-    _like(q, "q", bf16, (B, H, S_q, D), dev)
-    _like(k, "k", bf16, (B, H_kv, S_kv, D), dev)
-    _like(v, "v", bf16, (B, H_kv, S_kv, D), dev)
+    B, H, S_q, D = shape
+    H_kv, S_kv = kshape[1], kshape[2]
+    if not (q.dtype is bf16 and k.dtype is bf16 and v.dtype is bf16 and k.device == dev and v.device == dev
+            and v.shape == kshape and kshape[0] == B and kshape[3] == D and q.is_contiguous() and k.is_contiguous()
+            and v.is_contiguous()):
+        raise ValueError("q, k, v: contiguous bf16 tensors [B, H, S_q, D], [B, H_kv, S_kv, D] twice, on one device")
+    slp = stp = prp = qdp = kdp = lp = wp = None
     if slopes is not None:
         _like(slopes, "slopes", torch.float32, (H,), dev)
-    for t, name, shape in ((q_start, "q_start", (B,)), (prefix, "prefix", (B,)), (q_doc, "q_doc", (B, S_q)),
-                           (kv_doc, "kv_doc", (B, S_kv))):
-        if t is not None:
-            _like(t, name, i32, shape, dev)
-    out = torch.empty_like(q)
-    lse = torch.empty((B, H, S_q), dtype=torch.float32, device=dev) if with_lse else None
+        slp = slopes.data_ptr()
+    if q_start is not None:
+        _like(q_start, "q_start", torch.int32, (B,), dev)
+        stp = q_start.data_ptr()
+    if prefix is not None:
+        _like(prefix, "prefix", torch.int32, (B,), dev)
+        prp = prefix.data_ptr()
+    if q_doc is not None or kv_doc is not None:
+        _need(q_doc is not None and kv_doc is not None, "q_doc, kv_doc: both or neither")
+        _like(q_doc, "q_doc", torch.int32, (B, S_q), dev)
+        _like(kv_doc, "kv_doc", torch.int32, (B, S_kv), dev)
+        qdp, kdp = q_doc.data_ptr(), kv_doc.data_ptr()
+    out, lse = torch.empty_like(q), None
+    if with_lse:
+        lse = q.new_empty((B, H, S_q), dtype=torch.float32)
+        lp = lse.data_ptr()
     n = lib.dit_attn_masked_workspace_bytes(B, H, H_kv, S_q, S_kv, D, 0 if q_doc is None else 1)
-    ws = torch.empty((n,), dtype=torch.uint8, device=dev) if n else None
-    _check(lib.dit_attn_fwd_masked(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse), B, H, H_kv, S_q,
-                                   S_kv, D, 1.0 / D ** 0.5 if scale is None else scale, softcap, _ptr(slopes),
-                                   1 if causal else 0, _ptr(q_start), _ptr(prefix), _ptr(q_doc), _ptr(kv_doc), _ptr(ws),
-                                   n, _raw_stream(dev)), "dit_attn_fwd_masked")
+    if n:
+        ws = q.new_empty((n,), dtype=torch.uint8)
+        wp = ws.data_ptr()
+    rc = lib.dit_attn_fwd_masked(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lp, B, H, H_kv, S_q, S_kv, D,
+                                 1.0 / D ** 0.5 if scale is None else scale, softcap, slp, 1 if causal else 0, stp, prp,
+                                 qdp, kdp, wp, n, _raw_stream(dev.index))
+    if rc:
+        raise DitError(rc, "dit_attn_fwd_masked")
     return out, lse

@@ -396,7 +396,30 @@ struct MaskedCfg {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
-// tanh(x) = x p(x^2) for |x| <= 1, relative error 6e-7 (fit_tanh_poly.py), on the FMA pipe.
+// Capping by tanh(x) = x p(x^2) on the FMA pipe (fit_tanh_poly.py; relative error 6e-7), whose packed instructions it
+// keeps busy 2 cycles each: the FMA pipe bounds a capped call.  For |x| <= 1/2, the usual case, with p of degree 3 and
+// x = s c folded into its coefficients (k[i] = p_i c^(2i + 1)): five instructions a pair of scores.  Returns the
+// largest s^2.
+__device__ __forceinline__ float cap_small(uint32_t (&s)[128], const float (&k)[4]) {
+  float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 64; ++i) {
+    const uint64_t x = f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+    const uint64_t t = f2_mul(x, x);
+    uint64_t r = f2_fma(f2_pack(k[3], k[3]), t, f2_pack(k[2], k[2]));
+    r = f2_fma(r, t, f2_pack(k[1], k[1]));
+    r = f2_fma(r, t, f2_pack(k[0], k[0]));
+    float a, b, t0, t1;
+    f2_unpack(t, t0, t1);
+    m[i & 3] = fmax3(m[i & 3], t0, t1);
+    f2_unpack(f2_mul(x, r), a, b);
+    s[2 * i] = __float_as_uint(a);
+    s[2 * i + 1] = __float_as_uint(b);
+  }
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// The same for |x| <= 1 with p of degree 5.
 __device__ __forceinline__ uint64_t tanh_poly2(uint64_t x) {
   const uint64_t t = f2_mul(x, x);
   uint64_t r = f2_fma(f2_pack(-0.003067060373723507f, -0.003067060373723507f), t,
@@ -413,13 +436,12 @@ __device__ __forceinline__ float tanh_any(float x) {
   return 1.0f - __fdividef(2.0f, 1.0f + ex2_approx(x * 2.8853900817779268f));
 }
 
-// N scores s -> tanh(s * c), in place (the caller's unit becomes the cap).  The polynomial where every
-// |s * c| <= 1 in the warp, the usual case: capping is meant for rare large scores.
-template <int N>
-__device__ __forceinline__ void cap_scores(uint32_t (&s)[N], float c) {
+// Scores s -> tanh(s * c), in place, any size (the caller's unit becomes the cap): the polynomial where every
+// |s * c| <= 1 in the warp, else by exponentials.
+__device__ __forceinline__ void cap_scores(uint32_t (&s)[128], float c) {
   float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int i = 0; i < N; i += 8)
+  for (int i = 0; i < 128; i += 8)
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       m[k] = fmax3(m[k], fabsf(__uint_as_float(s[i + 2 * k])), fabsf(__uint_as_float(s[i + 2 * k + 1])));
@@ -427,7 +449,7 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[N], float c) {
   if (!__any_sync(0xffffffffu, far)) {
     const uint64_t c2 = f2_pack(c, c);
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
+    for (int i = 0; i < 128; i += 2) {
       float a, b;
       f2_unpack(tanh_poly2(f2_mul(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2)), a, b);
       s[i] = __float_as_uint(a);
@@ -435,12 +457,41 @@ __device__ __forceinline__ void cap_scores(uint32_t (&s)[N], float c) {
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = __float_as_uint(tanh_any(__uint_as_float(s[i]) * c));
+    for (int i = 0; i < 128; ++i) s[i] = __float_as_uint(tanh_any(__uint_as_float(s[i]) * c));
   }
 }
 
-// MOD: what is done to the scores, fixed at compile time because the softmax's registers are full: 0 nothing,
-// 1 the cap, 2 the distance bias and, where given, the cap.
+// cap_small and the exponentials in one pass, so that the one's FMA work runs under the other's special-function work:
+// p = 2^(cl * tanh(s c) - mc), the P words and the row sum; returns the largest s^2.
+__device__ __forceinline__ float cap_exp_pass(const uint32_t (&s)[128], const float (&k)[4], float cl, float mc,
+                                              uint32_t (&pw)[64], float& sum) {
+  float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const uint64_t cl2 = f2_pack(cl, cl), nmc2 = f2_pack(-mc, -mc);
+  uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+  for (int i = 0; i < 64; ++i) {
+    const uint64_t x = f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+    const uint64_t t = f2_mul(x, x);
+    uint64_t r = f2_fma(f2_pack(k[3], k[3]), t, f2_pack(k[2], k[2]));
+    r = f2_fma(r, t, f2_pack(k[1], k[1]));
+    r = f2_fma(r, t, f2_pack(k[0], k[0]));
+    float a, b, t0, t1;
+    f2_unpack(t, t0, t1);
+    m[i & 3] = fmax3(m[i & 3], t0, t1);
+    f2_unpack(f2_fma(f2_mul(x, r), cl2, nmc2), a, b);
+    a = ex2_approx(a);
+    b = ex2_approx(b);
+    acc[i & 3] = f2_add(acc[i & 3], f2_pack(a, b));
+    pw[i] = pack_bf16x2(a, b);
+  }
+  float lo, hi;
+  f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), lo, hi);
+  sum = lo + hi;
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// MOD: what is done to the scores, fixed at compile time because the softmax's registers are full: 1 the cap, 2 the
+// distance bias (3 both).
 template <int D, bool SPLIT, int MOD>
 __global__ void __launch_bounds__(384, 1)
     attn_masked_kernel(const __grid_constant__ MapSet<1> maps, const MaskedParams p) {
@@ -843,10 +894,26 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t tO = tmem_base + lane_off + (t ? C::kColO1 : C::kColO0);
     // one unit of the scores that the softmax sees, in natural-log and in log2 units: raw q.k, or
     // tanh(q.k * scale / cap)
-    const bool capped = MOD == 1 || (MOD == 2 && p.cap > 0.0f);
+    const bool capped = (MOD & 1) && p.cap > 0.0f;             // (split form: one kernel for every change)
     const float unit = capped ? p.cap : p.scale;
     const float cl = unit * 1.4426950408889634f;
     const float cap_c = capped ? p.scale / p.cap : 0.0f;
+    const float c2 = cap_c * cap_c;
+    const float cap_k[4] = {0.999999463558197f * cap_c, -0.33326318860054016f * cap_c * c2,
+                            0.13190296292304993f * cap_c * c2 * c2, -0.04440222680568695f * cap_c * c2 * c2 * c2};
+    const bool cap_folds = cap_c > 2e-5f && cap_c < 2e5f;        // (c^7 within fp32's range)
+    // S of this stream's tile, capped
+    auto load_s = [&](uint32_t (&s)[128]) {
+      tmem_ld128_sync(tS, s);
+      if (capped) {
+        if (cap_folds) {
+          const float t = cap_small(s, cap_k);
+          if (__all_sync(0xffffffffu, t * c2 <= 0.25f)) return;
+          tmem_ld128_sync(tS, s);
+        }
+        cap_scores(s, cap_c);
+      }
+    };
     bool ok = true;
     int g = 0, ns = 0, no = 0;                   // running tiles of the CTA, S tiles and O's of this stream
 
@@ -868,7 +935,7 @@ __global__ void __launch_bounds__(384, 1)
         if (p.words != nullptr) q.doc = max(__ldg(p.q_doc + static_cast<size_t>(b) * p.S_q + token), -2);
         if (q.doc == -1) q.doc = -2;
         q.lim = masked_limit(p, q.pos, info[7]);
-        if (MOD == 2 && p.slopes != nullptr)
+        if ((MOD & 2) && p.slopes != nullptr)
           q.slope = __ldg(p.slopes + (run - b * per_b) * p.run_heads + q.r / p.S_q) / unit;
       }
       return q;
@@ -997,9 +1064,8 @@ __global__ void __launch_bounds__(384, 1)
             uint32_t s[128], pw[64];
             float sum = 0.0f, alpha = 1.0f;
             bool need = false;
-            tmem_ld128_sync(tS, s);
-            if (capped) cap_scores(s, cap_c);
-            if (MOD == 2) {
+            load_s(s);
+            if (MOD & 2) {
               const float df = static_cast<float>(pos - j * kMaskedTile);
 #pragma unroll
               for (int c = 0; c < 128; ++c)
@@ -1036,17 +1102,26 @@ __global__ void __launch_bounds__(384, 1)
             float sum = 0.0f, alpha = 1.0f, off = 0.0f;
             bool need = false;
             auto scores = [&] {
-              tmem_ld128_sync(tS, s);
-              if (capped) cap_scores(s, cap_c);
-              if (MOD == 2) off = tilt_scores(s, pos - j * kMaskedTile);
+              load_s(s);
+              if (MOD & 2) off = tilt_scores(s, pos - j * kMaskedTile);
             };
-            scores();
+            // speculative pass, as in the dense form: the running maximum, kept when the row sums stay bounded
             bool slow = !started;
-            if (!slow) {
-              // speculative pass, as in the dense form: the running maximum, kept when the row sums stay bounded
-              exp_pass<false, 0>(s, cl, (m_use - off) * cl, pw, sum);
-              slow = __any_sync(0xffffffffu, !(sum <= C::kSumBound));
+            if constexpr (MOD == 1) {
+              slow |= !cap_folds;
+              if (!slow) {
+                tmem_ld128_sync(tS, s);
+                const float t = cap_exp_pass(s, cap_k, cl, m_use * cl, pw, sum);
+                slow = __any_sync(0xffffffffu, !(sum <= C::kSumBound && t * c2 <= 0.25f));
+              }
               if (slow) scores();
+            } else {
+              scores();
+              if (!slow) {
+                exp_pass<false, 0>(s, cl, (m_use - off) * cl, pw, sum);
+                slow = __any_sync(0xffffffffu, !(sum <= C::kSumBound));
+                if (slow) scores();
+              }
             }
             if (slow) exact(s, off, pw, sum, alpha, need);
             give(pw, sum, alpha, need);

@@ -1219,7 +1219,9 @@ int dit_attn_fwd_masked(const void* q, const void* k, const void* v, void* out, 
   if (plan.split && slopes == nullptr && softcap == 0.0f)
     return D == 64 ? launch_masked<64, true, 0>(q, k, v, prm, st) : launch_masked<128, true, 0>(q, k, v, prm, st);
   if (plan.split)
-    return D == 64 ? launch_masked<64, true, 2>(q, k, v, prm, st) : launch_masked<128, true, 2>(q, k, v, prm, st);
+    return D == 64 ? launch_masked<64, true, 3>(q, k, v, prm, st) : launch_masked<128, true, 3>(q, k, v, prm, st);
+  if (slopes != nullptr && softcap > 0.0f)
+    return D == 64 ? launch_masked<64, false, 3>(q, k, v, prm, st) : launch_masked<128, false, 3>(q, k, v, prm, st);
   if (slopes != nullptr)
     return D == 64 ? launch_masked<64, false, 2>(q, k, v, prm, st) : launch_masked<128, false, 2>(q, k, v, prm, st);
   if (softcap > 0.0f)
