@@ -45,6 +45,8 @@ struct MaskedParams {
   float* lse;                       // [B, H, S_q] or null
   int B, H, H_kv, S_q, S_kv;
   float scale, cap;                 // cap 0: scores not capped
+  float2 cap_k[6];                  // coefficients of the cap's polynomial in s, twice each (see cap_fold)
+  float cap_c, cap_limit;           // scale / cap; largest (s c)^2 that the polynomial is used for, < 0: never
   const float* slopes;              // [H] or null
   int causal;
   const int* q_start;               // [B] or null: S_kv - S_q
@@ -396,89 +398,68 @@ struct MaskedCfg {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
-// Capping by tanh(x) = x p(x^2) on the FMA pipe (fit_tanh_poly.py; relative error 6e-7), whose packed instructions it
-// keeps busy 2 cycles each: the FMA pipe bounds a capped call.  For |x| <= 1/2, the usual case, with p of degree 3 and
-// x = s c folded into its coefficients (k[i] = p_i c^(2i + 1)): five instructions a pair of scores.  Returns the
-// largest s^2.
-__device__ __forceinline__ float cap_small(uint32_t (&s)[128], const float (&k)[4]) {
+// Capping, tanh(x) with x = s c, c = scale / cap: x p(x^2) with p of degree 5 where every |x| <= 1 in the warp's tile
+// (fit_tanh_poly.py; relative error 6e-7), the usual case, since a cap is meant for rare large scores; else by
+// exponentials.  The polynomial runs on the FMA pipe, whose packed instructions take it 2 cycles each, while the
+// special-function unit is busy with the softmax's exponentials; c is folded into the coefficients, k[i] = p_i
+// c^(2i + 1), which saves one instruction a pair.  They come as kernel parameters, doubled for the packed
+// instructions, and so take no registers.  Powers of a small c leave fp32's range: from 5e-4 down |x| <= 1/4 is
+// asked for, where c^9 and c^11 do not matter, and below 5e-6 (c^7) the exponentials take over.
+inline void cap_fold(MaskedParams& p) {
+  const double poly[6] = {0.9999994039535522, -0.3332904279232025,  0.13281433284282684,
+                          -0.051605675369501114, 0.016743116080760956, -0.003067060373723507};
+  const double c = p.cap > 0.0f ? static_cast<double>(p.scale) / p.cap : 0.0;
+  double f = c;
+  for (int i = 0; i < 6; ++i, f *= c * c) p.cap_k[i] = make_float2(static_cast<float>(poly[i] * f), static_cast<float>(poly[i] * f));
+  p.cap_c = static_cast<float>(c);
+  p.cap_limit = c > 5e-4 && c < 1e3 ? 1.0f : (c > 5e-6 && c < 1e3 ? 0.0625f : -1.0f);
+}
+__device__ __forceinline__ uint64_t cap_coef(const MaskedParams& p, int i) { return f2_pack(p.cap_k[i].x, p.cap_k[i].y); }
+
+// tanh of a pair of scores; t = the pair's squares.
+__device__ __forceinline__ uint64_t cap_pair(uint64_t x, const MaskedParams& p, uint64_t& t) {
+  t = f2_mul(x, x);
+  uint64_t r = cap_coef(p, 5);
+#pragma unroll
+  for (int i = 4; i >= 0; --i) r = f2_fma(r, t, cap_coef(p, i));
+  return f2_mul(x, r);
+}
+
+// By the exponential, any x: 1 - 2 / (1 + e^2x), within 3e-7 absolutely.
+__device__ __forceinline__ float tanh_any(float x) {
+  return 1.0f - __fdividef(2.0f, 1.0f + ex2_approx(x * 2.8853900817779268f));
+}
+
+// Scores s -> tanh(s c) in place by the polynomial (the caller's unit becomes the cap); returns the largest s^2.
+__device__ __forceinline__ float cap_poly(uint32_t (&s)[128], const MaskedParams& p) {
   float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < 64; ++i) {
-    const uint64_t x = f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-    const uint64_t t = f2_mul(x, x);
-    uint64_t r = f2_fma(f2_pack(k[3], k[3]), t, f2_pack(k[2], k[2]));
-    r = f2_fma(r, t, f2_pack(k[1], k[1]));
-    r = f2_fma(r, t, f2_pack(k[0], k[0]));
+    uint64_t t;
     float a, b, t0, t1;
+    f2_unpack(cap_pair(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), p, t), a, b);
     f2_unpack(t, t0, t1);
     m[i & 3] = fmax3(m[i & 3], t0, t1);
-    f2_unpack(f2_mul(x, r), a, b);
     s[2 * i] = __float_as_uint(a);
     s[2 * i + 1] = __float_as_uint(b);
   }
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// The same for |x| <= 1 with p of degree 5.
-__device__ __forceinline__ uint64_t tanh_poly2(uint64_t x) {
-  const uint64_t t = f2_mul(x, x);
-  uint64_t r = f2_fma(f2_pack(-0.003067060373723507f, -0.003067060373723507f), t,
-                      f2_pack(0.016743116080760956f, 0.016743116080760956f));
-  r = f2_fma(r, t, f2_pack(-0.051605675369501114f, -0.051605675369501114f));
-  r = f2_fma(r, t, f2_pack(0.13281433284282684f, 0.13281433284282684f));
-  r = f2_fma(r, t, f2_pack(-0.3332904279232025f, -0.3332904279232025f));
-  r = f2_fma(r, t, f2_pack(0.9999994039535522f, 0.9999994039535522f));
-  return f2_mul(x, r);
-}
-
-// tanh by the exponential, any x: 1 - 2 / (1 + e^2x), within 3e-7 absolutely.
-__device__ __forceinline__ float tanh_any(float x) {
-  return 1.0f - __fdividef(2.0f, 1.0f + ex2_approx(x * 2.8853900817779268f));
-}
-
-// Scores s -> tanh(s * c), in place, any size (the caller's unit becomes the cap): the polynomial where every
-// |s * c| <= 1 in the warp, else by exponentials.
-__device__ __forceinline__ void cap_scores(uint32_t (&s)[128], float c) {
-  float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < 128; i += 8)
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      m[k] = fmax3(m[k], fabsf(__uint_as_float(s[i + 2 * k])), fabsf(__uint_as_float(s[i + 2 * k + 1])));
-  const bool far = !(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c <= 1.0f);
-  if (!__any_sync(0xffffffffu, far)) {
-    const uint64_t c2 = f2_pack(c, c);
-#pragma unroll
-    for (int i = 0; i < 128; i += 2) {
-      float a, b;
-      f2_unpack(tanh_poly2(f2_mul(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2)), a, b);
-      s[i] = __float_as_uint(a);
-      s[i + 1] = __float_as_uint(b);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 128; ++i) s[i] = __float_as_uint(tanh_any(__uint_as_float(s[i]) * c));
-  }
-}
-
-// cap_small and the exponentials in one pass, so that the one's FMA work runs under the other's special-function work:
+// The same and the exponentials in one pass, so that the one's FMA work runs under the other's special-function work:
 // p = 2^(cl * tanh(s c) - mc), the P words and the row sum; returns the largest s^2.
-__device__ __forceinline__ float cap_exp_pass(const uint32_t (&s)[128], const float (&k)[4], float cl, float mc,
+__device__ __forceinline__ float cap_exp_pass(const uint32_t (&s)[128], const MaskedParams& p, float cl, float mc,
                                               uint32_t (&pw)[64], float& sum) {
   float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   const uint64_t cl2 = f2_pack(cl, cl), nmc2 = f2_pack(-mc, -mc);
   uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
   for (int i = 0; i < 64; ++i) {
-    const uint64_t x = f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-    const uint64_t t = f2_mul(x, x);
-    uint64_t r = f2_fma(f2_pack(k[3], k[3]), t, f2_pack(k[2], k[2]));
-    r = f2_fma(r, t, f2_pack(k[1], k[1]));
-    r = f2_fma(r, t, f2_pack(k[0], k[0]));
+    uint64_t t;
     float a, b, t0, t1;
+    f2_unpack(f2_fma(cap_pair(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), p, t), cl2, nmc2), a, b);
     f2_unpack(t, t0, t1);
     m[i & 3] = fmax3(m[i & 3], t0, t1);
-    f2_unpack(f2_fma(f2_mul(x, r), cl2, nmc2), a, b);
     a = ex2_approx(a);
     b = ex2_approx(b);
     acc[i & 3] = f2_add(acc[i & 3], f2_pack(a, b));
@@ -897,21 +878,19 @@ __global__ void __launch_bounds__(384, 1)
     const bool capped = (MOD & 1) && p.cap > 0.0f;             // (split form: one kernel for every change)
     const float unit = capped ? p.cap : p.scale;
     const float cl = unit * 1.4426950408889634f;
-    const float cap_c = capped ? p.scale / p.cap : 0.0f;
-    const float c2 = cap_c * cap_c;
-    const float cap_k[4] = {0.999999463558197f * cap_c, -0.33326318860054016f * cap_c * c2,
-                            0.13190296292304993f * cap_c * c2 * c2, -0.04440222680568695f * cap_c * c2 * c2 * c2};
-    const bool cap_folds = cap_c > 2e-5f && cap_c < 2e5f;        // (c^7 within fp32's range)
+    // (s c)^2 within the polynomial's range, for the largest s^2 of each row of the warp
+    auto cap_fits = [&](float t) { return t * p.cap_c * p.cap_c <= p.cap_limit; };
     // S of this stream's tile, capped
     auto load_s = [&](uint32_t (&s)[128]) {
       tmem_ld128_sync(tS, s);
       if (capped) {
-        if (cap_folds) {
-          const float t = cap_small(s, cap_k);
-          if (__all_sync(0xffffffffu, t * c2 <= 0.25f)) return;
+        if (p.cap_limit > 0.0f) {
+          const float t = cap_poly(s, p);
+          if (__all_sync(0xffffffffu, cap_fits(t))) return;
           tmem_ld128_sync(tS, s);
         }
-        cap_scores(s, cap_c);
+#pragma unroll
+        for (int k = 0; k < 128; ++k) s[k] = __float_as_uint(tanh_any(__uint_as_float(s[k]) * p.cap_c));
       }
     };
     bool ok = true;
@@ -1108,11 +1087,11 @@ __global__ void __launch_bounds__(384, 1)
             // speculative pass, as in the dense form: the running maximum, kept when the row sums stay bounded
             bool slow = !started;
             if constexpr (MOD == 1) {
-              slow |= !cap_folds;
+              slow |= !(p.cap_limit > 0.0f);
               if (!slow) {
                 tmem_ld128_sync(tS, s);
-                const float t = cap_exp_pass(s, cap_k, cl, m_use * cl, pw, sum);
-                slow = __any_sync(0xffffffffu, !(sum <= C::kSumBound && t * c2 <= 0.25f));
+                const float t = cap_exp_pass(s, p, cl, m_use * cl, pw, sum);
+                slow = __any_sync(0xffffffffu, !(sum <= C::kSumBound && cap_fits(t)));
               }
               if (slow) scores();
             } else {

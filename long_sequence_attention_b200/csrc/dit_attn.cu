@@ -1201,6 +1201,7 @@ int dit_attn_fwd_masked(const void* q, const void* k, const void* v, void* out, 
   prm.lse = lse;
   prm.B = B; prm.H = H; prm.H_kv = H_kv; prm.S_q = S_q; prm.S_kv = S_kv;
   prm.scale = scale; prm.cap = softcap;
+  cap_fold(prm);
   prm.slopes = slopes; prm.causal = causal != 0; prm.q_start = q_start; prm.prefix = prefix;
   prm.q_doc = q_doc; prm.kv_doc = kv_doc;
   prm.rows = plan.rows; prm.n_blk = plan.n_blk; prm.n_split = plan.n_split; prm.n_units = static_cast<int>(plan.units);
