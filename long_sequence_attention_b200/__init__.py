@@ -16,6 +16,7 @@ only allocate outputs with torch and call the C entry points.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence, Tuple
 
@@ -431,7 +432,10 @@ def _raw_stream(index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index)
 
 
-_ll3, _i3 = ctypes.c_longlong * 3, ctypes.c_int * 3
+@functools.lru_cache(maxsize=1024)
+def _host_array(kind, *values):
+    """A small array of host numbers for a call to read (by value: the same numbers share one)."""
+    return (kind * len(values))(*values)
 
 
 def _need(ok: bool, what: str) -> None:
@@ -476,10 +480,12 @@ def rms_norm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None, g
         ldx = x.stride(0)
     wp = rp = hp = dp = h = ds = None
     if weight is not None:
-        _like(weight, "weight", dt, (C,), dev)
+        if weight.dtype is not dt or weight.shape != (C,) or weight.device != dev or not weight.is_contiguous():
+            _like(weight, "weight", dt, (C,), dev)
         wp = weight.data_ptr()
     if residual is not None:
-        _like(residual, "residual", dt, shape, dev)
+        if residual.dtype is not dt or residual.shape != shape or residual.device != dev or not residual.is_contiguous():
+            _like(residual, "residual", dt, shape, dev)
         rp = residual.data_ptr()
         h = residual if inplace else torch.empty_like(residual)
         hp = h.data_ptr()
@@ -595,8 +601,10 @@ def rope_qk(q, k, pos, freqs, q_weight=None, k_weight=None, eps: float = 1e-6, a
         if k is not None:
             dk = q.new_empty((B, H_kv, (S + 127) // 128), dtype=torch.float32)
             dkp = dk.data_ptr()
-    rc = lib.dit_rope_qk(q.data_ptr(), kp, _ll3(*qs[:3]), None if k is None else _ll3(*ks[:3]), qw, kw, eps, pos.data_ptr(),
-                         S * axes if B > 1 and ps[0] == B else 0, freqs.data_ptr(), (_i3)(*per), axes, 2 * pairs,
+    ll = ctypes.c_longlong
+    rc = lib.dit_rope_qk(q.data_ptr(), kp, _host_array(ll, *qs[:3]), None if k is None else _host_array(ll, *ks[:3]), qw, kw,
+                         eps, pos.data_ptr(),
+                         S * axes if B > 1 and ps[0] == B else 0, freqs.data_ptr(), _host_array(ctypes.c_int, *per), axes, 2 * pairs,
                          1 if interleaved else 0, magnitude, q_out.data_ptr(), kop, dqp, dkp, B, S, H, H_kv, D, code,
                          _raw_stream(dev.index))
     if rc:
