@@ -621,7 +621,6 @@ __global__ void __launch_bounds__(384, 1)
             const bool masked = ahead_masked;
             more = walk.next(ahead, ahead_run, ahead_masked);
             if (!(ok = put(note | (more ? 0 : kNoteLast), w.run, run, masked))) break;
-            if (masked && !(ok = put_v(note, w.b))) break;
             const int step = run < 0 ? -1 : 1;
             for (int j = note & kNoteTile; run != 0; j += step, run -= step) {
               const int st = g % NS;
@@ -644,6 +643,9 @@ __global__ void __launch_bounds__(384, 1)
                 ++nq;
               }
               if (g >= NS && !(ok = mbar_wait(bar_v_empty + st, ((g / NS) + 1) & 1, abort_flag, tmo, 0x22))) break;
+              // (only now: the V warps wait on bar_v_full of masked tiles alone, and the phase before this tile's has to
+              // be over when they do, or they would take that one for it)
+              if (masked && !(ok = put_v(note, w.b))) break;
               mbar_arrive_expect_tx(bar_v_full + st, C::kTileBytes);
               for (int b = 0; b < C::kNBlk; ++b)
                 tma_load_4d(sV + st * C::kTileBytes + b * C::kBlkBytes, &maps.v[0], bar_v_full + st, b * 64,
