@@ -387,7 +387,7 @@ int launch_rope(const RopeParams& prm, bool e4m3, cudaStream_t st) {
     const long long blocks = static_cast<long long>(prm.B) * ((prm.S + kRopeBlockRows - 1) / kRopeBlockRows);
     const int per = rope_heads_per(blocks, heads, 148 * RopeBlock<D>::kCtas);
     const dim3 grid(static_cast<unsigned>(blocks), (heads + per - 1) / per);
-    rope_e4m3_kernel<D, INTER><<<grid, 2 * kRopeThreads, RopeBlock<D>::kSmem, st>>>(prm, per);
+    rope_e4m3_kernel<D, INTER><<<grid, RopeBlock<D>::kThreads, RopeBlock<D>::kSmem, st>>>(prm, per);
   } else {
     constexpr int kTokens = kRopeThreads * 16 / D;
     const long long blocks = (static_cast<long long>(prm.B) * prm.S + kTokens - 1) / kTokens;

@@ -269,19 +269,20 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const RopeParams 
   }
 }
 
-// E4M3 out.  A CTA takes a block of 128 tokens and heads_per heads.  Its two halves of 256 threads take one head
-// each at a time: the block stays in registers between its maximum and its codes.  Both share the block's cosines and
-// sines in shared memory (64 KB at D = 128), and each has the next two heads' loads under way into shared memory
-// (asynchronous copies that only the thread that made them reads back, so that they need no barrier).
+// E4M3 out.  A CTA takes a block of 128 tokens and heads_per heads, one head at a time, one row piece of sixteen
+// elements a thread: it keeps its angles and, between the block's maximum and its codes, its results in registers.
+// The next heads' loads are under way into shared memory (asynchronous copies that only the thread that made them
+// reads back, so that they need no barrier); one barrier a head, for the maximum.  Issue slots bound it (about 165
+// instructions for sixteen elements), not bytes: 2 x 4429 x 48 x 128 take 47 us, 3.5 TB/s; with the angles in shared
+// memory and four row pieces a thread 49, with two heads' results in registers at a time more.
 constexpr int kRopeBlockRows = 128;
-constexpr int kRopeStages = 2;
+constexpr int kRopeStages = 3;
 template <int D>
 struct RopeBlock {
-  static constexpr int kLanes = D / 16, kRows = kRopeThreads / kLanes, kPass = kRopeBlockRows / kRows;
-  static constexpr int kPlanes = kRopeBlockRows * D / 2 * 8;    // four planes of float4: c, c', s, s' of a lane's pairs
+  static constexpr int kLanes = D / 16, kThreads = kRopeBlockRows * kLanes;
   static constexpr int kStage = kRopeBlockRows * D * 2;
-  static constexpr int kSmem = kPlanes + 2 * kRopeStages * kStage;   // 192 KB, D = 64: 96 KB
-  static constexpr int kCtas = 1;                               // on an SM (registers: 512 threads of 128)
+  static constexpr int kSmem = kRopeStages * kStage;
+  static constexpr int kCtas = 1024 / kThreads;                 // on an SM (registers: 1024 threads of 64)
 };
 
 __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
@@ -292,120 +293,120 @@ template <int N>
 __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <int D, bool INTER>
-__global__ void __launch_bounds__(2 * kRopeThreads, 1) rope_e4m3_kernel(const RopeParams p, int heads_per) {
+__global__ void __launch_bounds__(RopeBlock<D>::kThreads, RopeBlock<D>::kCtas) rope_e4m3_kernel(const RopeParams p, int heads_per) {
   using R = RopeBlock<D>;
-  constexpr int kLanes = R::kLanes, kRows = R::kRows, kPass = R::kPass, kPlane = kRopeBlockRows * kLanes;
-  extern __shared__ float4 planes[];
+  constexpr int kWarps = R::kThreads / 32;
+  extern __shared__ uint4 stages[];
   __shared__ RopeTable tab;
-  __shared__ float red[2][2][kRopeThreads / 32];
+  __shared__ float red[2][kWarps];
   rope_fill(p, tab);
-  const int half = threadIdx.x / kRopeThreads, tid = threadIdx.x % kRopeThreads;
   const int nblk = (p.S + kRopeBlockRows - 1) / kRopeBlockRows;
   const long long b = blockIdx.x / nblk;
   const int blk = blockIdx.x % nblk;
-  const int row0 = tid / kLanes, s0 = blk * kRopeBlockRows + row0;
-  const int lane = tid % kLanes;
-  const RopeLane r = rope_lane<D, INTER>(p.rot, lane);
+  const int s = blk * kRopeBlockRows + threadIdx.x / R::kLanes;
+  const bool on = s < p.S;
+  const RopeLane r = rope_lane<D, INTER>(p.rot, threadIdx.x % R::kLanes);
   const int first = blockIdx.y * heads_per, last = min(first + heads_per, p.heads[0] + p.heads[1]);
-  uint4* stage = reinterpret_cast<uint4*>(planes + R::kPlanes / 16) + half * kRopeStages * (R::kStage / 16) + tid;
-  // loads of this half's k-th head into stage k % kRopeStages: piece e of pass i at (2 i + e) * 256 + tid
-  auto load = [&](int k) {
-    const int hh = first + half + 2 * k;
-    if (hh < last) {
-      const int which = hh >= p.heads[0];
-      const __nv_bfloat16* x = p.x[which] + b * p.sb[which] + s0 * p.ss[which] + (which ? hh - p.heads[0] : hh) * p.sh[which];
-      uint4* dst = stage + (k % kRopeStages) * (R::kStage / 16);
-#pragma unroll
-      for (int i = 0; i < kPass; ++i)
-        if (s0 + i * kRows < p.S) {
-          copy_async16(dst + (2 * i) * kRopeThreads, x + i * kRows * p.ss[which] + r.lo);
-          copy_async16(dst + (2 * i + 1) * kRopeThreads, x + i * kRows * p.ss[which] + r.hi);
-        }
+  // running places of the next head to load and of the next to write, which go from q's heads to k's
+  const __nv_bfloat16* x;
+  uint8_t* out;
+  float* descale;
+  auto seek_x = [&](int which, int h) { x = p.x[which] + b * p.sb[which] + s * p.ss[which] + h * p.sh[which]; };
+  auto seek_out = [&](int which, int h) {
+    const long long bh = b * p.heads[which] + h;
+    out = static_cast<uint8_t*>(p.out[which]) + (bh * p.S + s) * D;
+    descale = p.descales[which] + bh * nblk + blk;
+  };
+  const int q_heads = p.heads[0];
+  seek_x(first >= q_heads, first >= q_heads ? first - q_heads : first);
+  seek_out(first >= q_heads, first >= q_heads ? first - q_heads : first);
+  uint4* const mine = stages + threadIdx.x;
+  int to_load = first, load_slot = 0;
+  auto load = [&] {
+    if (on && to_load < last) {
+      uint4* dst = mine + load_slot * (R::kStage / 16);
+      copy_async16(dst, x + r.lo);
+      copy_async16(dst + R::kThreads, x + r.hi);
     }
     copy_async_commit();
+    x += to_load < q_heads ? p.sh[0] : p.sh[1];
+    if (++to_load == q_heads && p.heads[1] > 0) seek_x(1, 0);
+    load_slot = load_slot == kRopeStages - 1 ? 0 : load_slot + 1;
   };
 #pragma unroll
-  for (int k = 0; k < kRopeStages; ++k) load(k);
-#pragma unroll 1
-  for (int i = half; i < kPass; i += 2) {
-    const int s = s0 + i * kRows;
+  for (int k = 0; k < kRopeStages; ++k) load();
+  uint64_t c2[4], s2[4];
+  {
     float c[8], sn[8];
-    rope_angles(p, tab, r, p.pos + b * p.pos_sb + static_cast<long long>(s) * p.axes, s < p.S, c, sn);
-    const int at = (row0 + i * kRows) * kLanes + lane;
-    planes[at] = make_float4(c[0], c[1], c[2], c[3]);
-    planes[kPlane + at] = make_float4(c[4], c[5], c[6], c[7]);
-    planes[2 * kPlane + at] = make_float4(sn[0], sn[1], sn[2], sn[3]);
-    planes[3 * kPlane + at] = make_float4(sn[4], sn[5], sn[6], sn[7]);
+    rope_angles(p, tab, r, p.pos + b * p.pos_sb + static_cast<long long>(s) * p.axes, on, c, sn);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      c2[k] = f2_pack(c[2 * k], c[2 * k + 1]);
+      s2[k] = f2_pack(sn[2 * k], sn[2 * k + 1]);
+    }
   }
-  __syncthreads();
-  int at_which = -1;
   RopeRaw w = {};
+  bool norm = false;
+  auto weights = [&](int which) {
+    norm = p.weight[which] != nullptr;
+    if (norm) w = rope_load(p.weight[which], r);
+  };
+  weights(first >= q_heads);
+  int slot = 0, flip = 0;
 #pragma unroll 1
-  for (int k = 0; first + half + 2 * k < last; ++k) {
-    const int hh = first + half + 2 * k, which = hh >= p.heads[0], h = which ? hh - p.heads[0] : hh;
-    const bool norm = p.weight[which] != nullptr;
-    if (norm && which != at_which) w = rope_load(p.weight[which], r);
-    at_which = which;
+  for (int hh = first; hh < last; ++hh) {
+    if (hh == q_heads && hh != first) {
+      weights(1);
+      seek_out(1, 0);
+    }
     copy_async_wait<kRopeStages - 1>();
-    const uint4* src = stage + (k % kRopeStages) * (R::kStage / 16);
-    uint64_t ya[kPass][4], yb[kPass][4];
+    RopeRaw raw = {};
+    if (on) raw = RopeRaw{mine[slot * (R::kStage / 16)], mine[slot * (R::kStage / 16) + R::kThreads]};
+    slot = slot == kRopeStages - 1 ? 0 : slot + 1;
+    uint64_t ya[4], yb[4];
+    rope_apply<D, INTER>(r, raw, norm, w, p.eps, c2, s2, ya, yb);
+    load();
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPass; ++i) {
-      RopeRaw raw = {};
-      if (s0 + i * kRows < p.S) raw = RopeRaw{src[(2 * i) * kRopeThreads], src[(2 * i + 1) * kRopeThreads]};
-      const int at = (row0 + i * kRows) * kLanes + lane;
-      const float4 ca = planes[at], cb = planes[kPlane + at], sa = planes[2 * kPlane + at], sb = planes[3 * kPlane + at];
-      const uint64_t c2[4] = {f2_pack(ca.x, ca.y), f2_pack(ca.z, ca.w), f2_pack(cb.x, cb.y), f2_pack(cb.z, cb.w)};
-      const uint64_t s2[4] = {f2_pack(sa.x, sa.y), f2_pack(sa.z, sa.w), f2_pack(sb.x, sb.y), f2_pack(sb.z, sb.w)};
-      rope_apply<D, INTER>(r, raw, norm, w, p.eps, c2, s2, ya[i], yb[i]);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float a0, a1, b0, b1;
-        f2_unpack(ya[i][q], a0, a1);
-        f2_unpack(yb[i][q], b0, b1);
-        m = fmax3(m, fabsf(a0), fabsf(a1));
-        m = fmax3(m, fabsf(b0), fabsf(b1));
-      }
+    for (int k = 0; k < 4; ++k) {
+      float a0, a1, b0, b1;
+      f2_unpack(ya[k], a0, a1);
+      f2_unpack(yb[k], b0, b1);
+      m = fmax3(m, fabsf(a0), fabsf(a1));
+      m = fmax3(m, fabsf(b0), fabsf(b1));
     }
-    load(k + kRopeStages);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((tid & 31) == 0) red[half][k & 1][tid >> 5] = m;
-    asm volatile("bar.sync %0, %1;" ::"r"(half + 1), "n"(kRopeThreads) : "memory");   // (this half's threads)
-    m = red[half][k & 1][tid & (kRopeThreads / 32 - 1)];       // (two buffers: one barrier a head is enough)
-#pragma unroll
-    for (int o = kRopeThreads / 64; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float d = m > 0.0f ? __fdiv_rn(m, 448.0f) : 1.0f;
+    // (of values >= 0 the bits order as the values do: one instruction for the warp's maximum)
+    m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+    if ((threadIdx.x & 31) == 0) red[flip][threadIdx.x >> 5] = m;
+    __syncthreads();
+    m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(red[flip][threadIdx.x & (kWarps - 1)])));
+    const float d = m > 0.0f ? __fdiv_rn(m, 448.0f) : 1.0f;     // (two buffers: one barrier a head is enough)
     const float rcp = __frcp_rn(d);
-    const long long bh = b * p.heads[which] + h;
-    if (tid == 0) p.descales[which][bh * nblk + blk] = m > 0.0f ? d : 0.0f;
-    uint8_t* out = static_cast<uint8_t*>(p.out[which]) + (bh * p.S + s0) * D;
+    if (threadIdx.x == 0) *descale = m > 0.0f ? d : 0.0f;
+    flip ^= 1;
     const uint64_t rcp2 = f2_pack(rcp, rcp);
+    uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < kPass; ++i) {
-      uint32_t c[4];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        float a0, a1, a2, a3, b0, b1, b2, b3;
-        f2_unpack(f2_mul(ya[i][2 * q], rcp2), a0, a1);
-        f2_unpack(f2_mul(ya[i][2 * q + 1], rcp2), a2, a3);
-        f2_unpack(f2_mul(yb[i][2 * q], rcp2), b0, b1);
-        f2_unpack(f2_mul(yb[i][2 * q + 1], rcp2), b2, b3);
-        if (INTER) {
-          c[2 * q] = pack_e4m3x4(a0, b0, a1, b1);
-          c[2 * q + 1] = pack_e4m3x4(a2, b2, a3, b3);
-        } else {
-          c[q] = pack_e4m3x4(a0, a1, a2, a3);
-          c[2 + q] = pack_e4m3x4(b0, b1, b2, b3);
-        }
-      }
-      if (s0 + i * kRows < p.S) {
-        uint8_t* dst = out + static_cast<long long>(i) * kRows * D;
-        *reinterpret_cast<uint2*>(dst + r.lo) = make_uint2(c[0], c[1]);
-        *reinterpret_cast<uint2*>(dst + r.hi) = make_uint2(c[2], c[3]);
+    for (int q = 0; q < 2; ++q) {
+      float a0, a1, a2, a3, b0, b1, b2, b3;
+      f2_unpack(f2_mul(ya[2 * q], rcp2), a0, a1);
+      f2_unpack(f2_mul(ya[2 * q + 1], rcp2), a2, a3);
+      f2_unpack(f2_mul(yb[2 * q], rcp2), b0, b1);
+      f2_unpack(f2_mul(yb[2 * q + 1], rcp2), b2, b3);
+      if (INTER) {
+        c[2 * q] = pack_e4m3x4(a0, b0, a1, b1);
+        c[2 * q + 1] = pack_e4m3x4(a2, b2, a3, b3);
+      } else {
+        c[q] = pack_e4m3x4(a0, a1, a2, a3);
+        c[2 + q] = pack_e4m3x4(b0, b1, b2, b3);
       }
     }
+    if (on) {
+      *reinterpret_cast<uint2*>(out + r.lo) = make_uint2(c[0], c[1]);
+      *reinterpret_cast<uint2*>(out + r.hi) = make_uint2(c[2], c[3]);
+    }
+    out += static_cast<long long>(p.S) * D;
+    descale += nblk;
   }
   copy_async_wait<0>();
 }
