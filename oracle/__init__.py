@@ -17,6 +17,9 @@ Contents
                    tiny shapes (``brute_attention.c``), used to pin ``attention``.
 ``neighborhood``   3-D neighborhood attention on a T x Y x X token grid (the NATTEN
                    na3d operation): clamped fixed-size windows, explicit softmax, fp64.
+``block``          root-mean-square norm with the residual's addition, rotary positions, and
+                   attention with capped scores, a distance bias and causal, prefix and
+                   document masks, fp64 (pinned by ``tests/test_oracle_block.py``).
 
 Parity status: every function here is pinned by ``tests/test_oracle.py`` (brute force,
 closed forms, invariants, a library cross-check and planted-mistake checks).
