@@ -19,7 +19,13 @@
  * --ring_degree).  An FP8-E4M3 input variant follows the FP8 attention backend named on the
  * AMD ROCm summary page (--attention_backend aiter_flydsl_fp8; "FP8 may change outputs").
  *
- * Conventions shared by every call
+ * Around it stand the operators of a block that read and write the same tensors: the norm with
+ * the residual's addition (dit_rms_norm), rotary positions of queries and keys (dit_rope_qk), and
+ * attention under masks, caps and biases, with few queries against a long cache as a case of its
+ * own (dit_attn_fwd_masked), for packed images of several sizes, padded text and generation
+ * after a prefix.
+ *
+ * Conventions shared by every call (where a call does not say otherwise)
  * --------------------------------
  *  - Tensors are dense row-major [B, H, S, D] (D innermost, stride 1); LSE arrays are fp32
  *    [B, H, S].  D must be 64 or 128.
@@ -314,7 +320,8 @@ int dit_quant_fp8_noalloc(const void* x_bf16, void* x_fp8, float* descale, long 
  *   residual  [rows, C] of dtype, or NULL (h = x).
  *   weight    [C] of dtype, or NULL (ones).
  *   out       [rows, C]: DIT_BF16, DIT_FP32, or DIT_FP8_E4M3 codes with scales:
- *             descale = max|y| / 448 (1 if the maximum is 0), code = rn_satfinite(y / descale).
+ *             descale = max|y| / 448 (1 if the maximum is below 2^-119), code = rn_satfinite(y / descale), the
+ *             quotient formed as y * (448 / max|y|) in fp32.
  *   group     E4M3: columns of one scale, 0 (the whole row) or 128 (the last group of a row
  *             may be shorter); otherwise 0.
  *   descales  E4M3: [rows, 1] or [rows, ceil(C/128)] fp32, written; otherwise NULL.
@@ -346,8 +353,9 @@ int dit_rms_norm(const void* x, long long x_stride, const void* residual, const 
  *             the axis whose run it falls in (t, y, x grids; axes = 1 for text).
  *   interleaved != 0: pair i is elements (2i, 2i + 1); 0: (i, i + rot / 2), rot a multiple of 16.
  *   q_out, k_out  [B, H, S, D], [B, H_kv, S, D]: DIT_BF16, or DIT_FP8_E4M3 codes in 128-row blocks
- *             with descales dq_blk [B, H, ceil(S/128)], dk_blk [B, H_kv, ceil(S/128)] by the rule of
- *             dit_quant_fp8_blocks, ready for dit_attn_fwd_fp8_blocks (bf16: descales NULL).
+ *             with descales dq_blk [B, H, ceil(S/128)], dk_blk [B, H_kv, ceil(S/128)] as those of
+ *             dit_quant_fp8_blocks (0 below 2^-119; of the unrounded results, the quotient as y * (448 / max|y|)), ready
+ *             for dit_attn_fwd_fp8_blocks (bf16: descales NULL).
  *   D = 64 or 128.  B * S = 0: nothing to do.
  */
 int dit_rope_qk(const void* q, const void* k, const long long* q_strides, const long long* k_strides,

@@ -31,6 +31,13 @@
 //   * The two idle warps of the dense form look through the V rows of tiles that are masked for some row: a
 //     non-finite value would reach every row of the tile (0 * inf), so it is zeroed in shared memory
 //     and its key flagged; the rows that may see that key become NaN, the others never notice.
+//
+// What bounds it: the hand-offs and the softmax of a tile, as in the dense form (205 us for 24 x 4608 x 128; here,
+// without masks, 219), with two softmax warps on a scheduler; a masked tile costs a stream 3.1 us where a whole one
+// costs 1.65 (D = 64), of which the mask's bits take 0.5 and their application 0.5.  B200, 24 x 4608 x 128: causal
+// 149 us, bias 248, bias and causal 163 (6 key heads), capped 305; 8(4) x 16896 x 128 causal after a prefix of 512:
+// 488 us, 1200 TFLOP/s of the pairs that the mask leaves; 2 x 24 x 4429 x 64 in seven documents 158 us; one query of
+// 4 x 40(8) heads x 32760 keys 90 us, 5.7 TB/s.
 #pragma once
 
 #include <cuda_bf16.h>

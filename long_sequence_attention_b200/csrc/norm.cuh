@@ -6,12 +6,14 @@
 // the stream h is rounded once to its type for the next layer, and y is rounded once from the
 // unrounded fp32 h (so the norm does not see the stream's rounding).  E4M3 output follows the
 // quantisers' rule per group of columns (a whole row, or 128 columns):
-//     descale = max |y| / 448 (1 if the maximum is 0),  code = e4m3_rn_satfinite(y / descale).
+//     descale = max |y| / 448 (1 if the maximum is below 2^-119),  code = e4m3_rn_satfinite(y / descale).
 //
 // Bytes bound: each element is read once (x, r) and written once (h, y).  So a row stays in registers
 // between the sum and the output: a CTA per row (or, up to 128 pieces of 16 bytes, 8 to 32 lanes of
 // a warp), NV 16-byte pieces a thread.  Rows that are not whole aligned 16-byte pieces are held as
-// single elements; rows too long for the registers are read again from the caches instead.
+// single elements; rows too long for the registers are read again from the caches instead.  B200, rows of
+// 5120 bf16 with a residual, 32760 of them: 172 us to E4M3 with a scale every 128 columns (6.8 TB/s), 197 us
+// to bf16 (6.8 TB/s); one such row 2.2 us; 40000 rows of 1000 to bf16 50 us, of 1001 (single elements) 99 us.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -20,6 +22,9 @@
 #include "quant.cuh"
 
 namespace dit {
+
+// Groups whose largest magnitude is below this count as zeros: 448 over it would leave fp32's range.
+constexpr float kE4m3Least = 1.504632769052528e-36f;   // 2^-119
 
 struct NormParams {
   const void* x;
@@ -81,7 +86,7 @@ struct NormVec<float> {
 };
 
 // N results to the output row at element e: bf16, fp32 (OUT 0, 1) or E4M3 codes of y / d (OUT 2), the quotient taken as
-// y times 1 / d correctly rounded: y carries roundings of that size anyhow.
+// y times 448 / max |y| (rcp), correctly rounded: y carries roundings of that size anyhow.
 template <int OUT, int N>
 __device__ __forceinline__ void norm_store(void* out, long long e, const float (&y)[N], float rcp) {
   if constexpr (OUT == 0) {
@@ -198,8 +203,8 @@ __global__ void __launch_bounds__(LANES ? 256 : (NV <= 2 ? 1024 : 512), LANES ||
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       }
     }
-    d = m > 0.0f ? __fdiv_rn(m, 448.0f) : 1.0f;
-    rcp = __frcp_rn(d);
+    d = m >= kE4m3Least ? __fdiv_rn(m, 448.0f) : 1.0f;
+    rcp = m >= kE4m3Least ? __fdiv_rn(448.0f, m) : 1.0f;
     if (on && at == 0) p.descales[row] = d;
   }
 #pragma unroll
@@ -214,8 +219,8 @@ __global__ void __launch_bounds__(LANES ? 256 : (NV <= 2 ? 1024 : 512), LANES ||
 #pragma unroll
       for (int o = (LANES && LANES < kGroup ? LANES : kGroup) / 2; o > 0; o >>= 1)
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      d = m > 0.0f ? __fdiv_rn(m, 448.0f) : 1.0f;
-      rcp = __frcp_rn(d);
+      d = m >= kE4m3Least ? __fdiv_rn(m, 448.0f) : 1.0f;
+      rcp = m >= kE4m3Least ? __fdiv_rn(448.0f, m) : 1.0f;
       if (on && v < nvec && v % kGroup == 0) p.descales[row * ((p.C + 127) / 128) + v / kGroup] = d;
     }
     if (on && v < nvec) norm_store<OUT, N>(p.out, base + v * N, h[i], rcp);
@@ -269,8 +274,8 @@ __global__ void __launch_bounds__(1024) rms_norm_cols_kernel(const NormParams p)
   float d = 1.0f, rcp = 1.0f;
   if (OUT == 2 && p.group == p.C) {
     row_m = block_max(row_m, red[1]);
-    d = row_m > 0.0f ? __fdiv_rn(row_m, 448.0f) : 1.0f;
-    rcp = __frcp_rn(d);
+    d = row_m >= kE4m3Least ? __fdiv_rn(row_m, 448.0f) : 1.0f;
+    rcp = row_m >= kE4m3Least ? __fdiv_rn(448.0f, row_m) : 1.0f;
     if (threadIdx.x == 0) p.descales[row] = d;
   }
 #pragma unroll
@@ -280,8 +285,8 @@ __global__ void __launch_bounds__(1024) rms_norm_cols_kernel(const NormParams p)
       float a = m[g];
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-      d = a > 0.0f ? __fdiv_rn(a, 448.0f) : 1.0f;
-      rcp = __frcp_rn(d);
+      d = a >= kE4m3Least ? __fdiv_rn(a, 448.0f) : 1.0f;
+      rcp = a >= kE4m3Least ? __fdiv_rn(448.0f, a) : 1.0f;
       if (lane == 0 && c0 < p.C) p.descales[row * ((p.C + 127) / 128) + c0 / 128] = d;
     }
 #pragma unroll
@@ -323,7 +328,7 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_kernel(const NormParams
         float m = 0.0f;
         for (int c = g * p.group + threadIdx.x; c < c1; c += kNormThreads) m = fmaxf(m, fabsf(y_at(c)));
         const float amax = block_max(m, red);
-        const float d = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+        const float d = amax >= kE4m3Least ? __fdiv_rn(amax, 448.0f) : 1.0f;
         if (threadIdx.x == 0) p.descales[row * ng + g] = d;
         for (int c = g * p.group + threadIdx.x; c < c1; c += kNormThreads)
           static_cast<uint8_t*>(p.out)[base + c] =

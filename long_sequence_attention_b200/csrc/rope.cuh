@@ -10,7 +10,7 @@
 // Angles in whole turns, 64-bit fixed point: F = freq / 2 pi * 2^64 mod 2^64, and position * F
 // in 64-bit integer arithmetic drops whole turns exactly, so far positions lose nothing.  Of the
 // fraction the nearest quarter turn comes off in integers too; cosine and sine of the rest, at most an
-// eighth of a turn, are polynomials (fit_rope_poly.py), within 2 * 2^-24 absolutely.
+// eighth of a turn, are polynomials (fit_rope_poly.py), within 1.1 * 2^-24 absolutely.
 //
 // Bytes bound: q and k are read once and written once.  Sixteen elements a lane, D / 16 lanes a head row; a
 // lane's sixteen are two runs of eight and hold eight whole pairs in either layout, so nothing crosses lanes but
@@ -58,16 +58,22 @@ __device__ __forceinline__ void rope_cos_sin(int pos, unsigned long long turns, 
   const uint32_t hi = static_cast<uint32_t>(t >> 32);           // in 2^-32 turns
   const uint32_t quarter = (hi + 0x20000000u) >> 30;
   const int rest = static_cast<int>(hi - (quarter << 30));      // in [-2^29, 2^29)
-  const float x = static_cast<float>(rest) * 4.6566128730773926e-10f;   // 2^-31: half turns, |x| <= 1/4
+  const float xi = static_cast<float>(rest);                    // 24 of its bits,
+  const float dx = static_cast<float>(rest - static_cast<int>(xi)) * 1.4629180792671596e-09f;   // and pi 2^-31 times the rest
+  const float x = xi * 4.6566128730773926e-10f;                 // 2^-31: half turns, |x| <= 1/4
   const float u = x * x;
-  float sp = fmaf(0.08099587261676788f, u, -0.5992013812065125f);
-  sp = fmaf(sp, u, 2.5501625537872314f);
-  sp = fmaf(sp, u, -5.167712688446045f);
-  sp = fmaf(sp, u, 3.1415927410125732f) * x;
+  float q = fmaf(0.08099587261676788f, u, -0.5992013812065125f);
+  q = fmaf(q, u, 2.5501625537872314f);
+  q = fmaf(q, u, -5.167712688446045f);
+  q = fmaf(q, u, -8.742277657347586e-08f);                      // pi less its fp32 value, which comes last
+  float sp = fmaf(x, 3.1415927410125732f, x * q);
   float cp = fmaf(0.23126092553138733f, u, -1.3350359201431274f);
   cp = fmaf(cp, u, 4.058706760406494f);
   cp = fmaf(cp, u, -4.934802055358887f);
   cp = fmaf(cp, u, 1.0f);
+  const float s0 = sp;
+  sp = fmaf(cp, dx, sp);
+  cp = fmaf(-s0, dx, cp);
   const float a = (quarter & 1u) ? sp : cp, b = (quarter & 1u) ? cp : sp;
   c = ((quarter + 1u) & 2u) ? -a * magnitude : a * magnitude;
   s = (quarter & 2u) ? -b * magnitude : b * magnitude;
@@ -380,9 +386,9 @@ __global__ void __launch_bounds__(RopeBlock<D>::kThreads, RopeBlock<D>::kCtas) r
     if ((threadIdx.x & 31) == 0) red[flip][threadIdx.x >> 5] = m;
     __syncthreads();
     m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(red[flip][threadIdx.x & (kWarps - 1)])));
-    const float d = m > 0.0f ? __fdiv_rn(m, 448.0f) : 1.0f;     // (two buffers: one barrier a head is enough)
-    const float rcp = __frcp_rn(d);
-    if (threadIdx.x == 0) *descale = m > 0.0f ? d : 0.0f;
+    const float d = m >= kE4m3Least ? __fdiv_rn(m, 448.0f) : 1.0f;     // (two buffers: one barrier a head is enough)
+    const float rcp = m >= kE4m3Least ? __fdiv_rn(448.0f, m) : 1.0f;   // (1 / d with one rounding less)
+    if (threadIdx.x == 0) *descale = m >= kE4m3Least ? d : 0.0f;
     flip ^= 1;
     const uint64_t rcp2 = f2_pack(rcp, rcp);
     uint32_t c[4];

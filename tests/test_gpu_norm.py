@@ -115,6 +115,18 @@ def test_large_and_small_magnitudes(cuda_lib):
         _check(y, None, block.rms_norm(_np(x), eps=0.0)[0], 640, 0)
 
 
+def test_e4m3_of_tiny_rows(cuda_lib):
+    """Down to 2^-119 the scale holds; below, a group counts as zeros (never NaN)."""
+    import torch
+    x = torch.zeros(4, 256, device="cuda")
+    x[0, 5], x[1, 200], x[2, 7], x[3] = 1e-30, -2e-36, 1e-37, 1e-44
+    for group in (0, 128):
+        c, _, d = cuda_lib.rms_norm(x, eps=1.0, out_dtype=torch.uint8, group=group)
+        back = c.view(torch.float8_e4m3fn).float().view(4, -1, 128) * d.view(4, -1, 1)
+        assert not torch.any(torch.isnan(back)) and torch.all(back[2:] == 0)
+        assert abs(back[0].max() / 1e-30 - 1) < 2.0 ** -4 and abs(back[1].min() / -2e-36 - 1) < 2.0 ** -4
+
+
 def test_streams_and_graph(cuda_lib):
     import torch
     x, r = _make((64, 5120), torch.bfloat16, 10), _make((64, 5120), torch.bfloat16, 11)
