@@ -1210,15 +1210,22 @@ __global__ void __launch_bounds__(128) masked_join_kernel(const MaskedParams p) 
   if (M != -INFINITY) {
     for (int c0 = 0; c0 < n; c0 += 32) {
       const float wl = c0 + lane < n ? __expf(p.part_lse[(c0 + lane) * n_rows + row] - M) : 0.0f;
-      const int m = min(32, n - c0);
-#pragma unroll 4
-      for (int k = 0; k < m; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, wl, k);
-        L += wk;
-        if (wk != 0.0f) {
-          const float* o = p.part_o + ((c0 + k) * n_rows + row) * D + lane * (D / 32);
+      // eight partials' loads in flight; what an empty share's holds is discarded by a select
+      for (int k0 = 0; k0 < min(32, n - c0); k0 += 8) {
+        float v[8][D / 32];
 #pragma unroll
-          for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(wk, o[e], acc[e]);
+        for (int k = 0; k < 8; ++k) {
+          const int c = min(c0 + k0 + k, n - 1);
+          const float* o = p.part_o + (c * n_rows + row) * D + lane * (D / 32);
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) v[k][e] = o[e];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, wl, k0 + k);
+          L += wk;
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) acc[e] = wk != 0.0f ? fmaf(wk, v[k][e], acc[e]) : acc[e];
         }
       }
     }
